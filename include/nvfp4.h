@@ -242,6 +242,45 @@ nvfp4_status nvfp4_fp8_gemm(const uint8_t *a_q, const float *a_g,
                             nvfp4_dtype c_type, int64_t ldc, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Block-scaled FP8 quantize: E4M3 codes with one FP32 scale per block of 128
+ * columns, over one row (activations) or 128 rows (weights).  The per-tensor
+ * quantizer above loses the small channels of a tensor whose channels differ
+ * widely; a scale per block keeps them.
+ *
+ * x       float32 or bfloat16 [rows][ld_x], ld_x >= cols (elements).
+ * block_rows  1 or 128: rows that share a scale.
+ * q       [rows][cols] E4M3FN codes, 16-byte aligned.
+ * s       float [ceil(rows/block_rows)][ceil(cols/128)] decode scales:
+ *         x_hat = e4m3(q) * s; blocks at the edges are shorter.
+ *   s = max(fl(amax/448), 2^-126), amax = max|x| of the block; 1 if amax == 0
+ *   q = the code nearest the exact quotient x/s (ties to even, sign of x kept).
+ * cols > 0, cols % 16 == 0, rows >= 0, rows * cols / 16 < 2^31.  No workspace.
+ * Alignment of x as for nvfp4_quantize (other layouts take a slower path).
+ * ---------------------------------------------------------------------- */
+nvfp4_status nvfp4_fp8_block_quantize(const void *x, nvfp4_dtype x_type,
+                                      int64_t rows, int64_t cols, int64_t ld_x,
+                                      int32_t block_rows, uint8_t *q, float *s,
+                                      hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Block-scaled FP8 GEMM (operands as nvfp4_fp8_block_quantize writes them).
+ *
+ *   C[m][n] = sum_b a_s[m][b] * b_s[n/128][b]
+ *                   * sum_{k = 128b .. 128b+127, k < K} e4m3(A[m][k]) e4m3(B[n][k])
+ * A [M x K] activations with scales [M][ceil(K/128)], B [N x K] weights (one
+ * row per output feature) with scales [ceil(N/128)][ceil(K/128)], dense
+ * row-major E4M3FN bytes, 16-byte aligned; scales finite.  Products inside a
+ * block are exact, accumulation is float32 over a block and over the blocks;
+ * the result is rounded to c_type.  M, N >= 0; K > 0, K % 16 == 0; c is
+ * [M][ldc] of c_type, ldc >= N, aligned to its element.
+ * ---------------------------------------------------------------------- */
+nvfp4_status nvfp4_fp8_block_gemm(const uint8_t *a_q, const float *a_s,
+                                  const uint8_t *b_q, const float *b_s,
+                                  int64_t M, int64_t N, int64_t K, void *c,
+                                  nvfp4_dtype c_type, int64_t ldc,
+                                  hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * MoE routing (two-level scaling page, section "Why only routed experts":
  * each token uses k of E routed experts chosen by a BF16 router).
  *
@@ -336,6 +375,45 @@ nvfp4_status nvfp4_moe_combine(const void *y, nvfp4_dtype y_type,
                                int64_t T, int32_t k, int64_t H, int64_t R,
                                void *out, nvfp4_dtype out_type,
                                hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The whole routed-expert layer for few tokens (a decode step): routing, gated
+ * expert products and combine in one call.
+ *
+ *   ids, w = as nvfp4_moe_route: top-k, softmax over the selected logits
+ *   h_j = SiLU(Wg[e_j] x) * (Wu[e_j] x);  out = sum_{j<k} w_j * Wd[e_j] h_j
+ * Weights are NVFP4; the activations x and h are NOT quantized (with few tokens
+ * the layer is bound by the selected experts' bytes, each read once), so the
+ * result is that of the dequantized weights in float32: h is carried to the
+ * full 24 bits when out is float32 and to 2^-18 when out is bfloat16.  For many
+ * tokens use the routed calls above.
+ *
+ * x       [T][ld_x] of x_type (f32 or bf16), ld_x >= H (elements).
+ * logits  float [T][E], dense.
+ * gu_q/gu_s/gu_g  expert weights [E][2I][H/2], [E][2I][H/16], [E]: rows [0, I)
+ *         the gate, [I, 2I) the up projection.
+ * d_q/d_s/d_g     [E][H][I/2], [E][H][I/16], [E].
+ * out     [T][ld_out] of out_type, ld_out >= H; must not overlap x.
+ * 1 <= k <= E <= 1024, k <= 32; H, I > 0, multiples of 16, <= 2^20.
+ * T >= 0; more than 128 tokens return NVFP4_ERR_UNSUPPORTED.
+ * Any alignment of x, out (their element's), q and s; the fastest path needs
+ * H % 64 == 0, I % 64 == 0, 16-byte aligned q and 4-byte aligned s.
+ * workspace  nvfp4_moe_decode_workspace_size(T, E, k, H, I) bytes, 256-byte
+ *         aligned, clobbered; contents on entry do not matter.  Calls that
+ *         overlap in time need separate workspaces.
+ * The summation order is fixed: equal calls give equal bits.
+ * ---------------------------------------------------------------------- */
+size_t nvfp4_moe_decode_workspace_size(int64_t T, int32_t E, int32_t k,
+                                       int64_t H, int64_t I);
+nvfp4_status nvfp4_moe_decode(const void *x, nvfp4_dtype x_type, int64_t ld_x,
+                              const float *logits, int64_t T, int32_t E,
+                              int32_t k, int64_t H, int64_t I,
+                              const uint8_t *gu_q, const uint8_t *gu_s,
+                              const float *gu_g, const uint8_t *d_q,
+                              const uint8_t *d_s, const float *d_g, void *out,
+                              nvfp4_dtype out_type, int64_t ld_out,
+                              void *workspace, size_t workspace_bytes,
+                              hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -26,7 +26,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnvfp4.so")
 ARCH = "gfx950"
 
-SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "fp8_gemm.hip", "moe.hip"]
+SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "fp8_gemm.hip", "moe.hip",
+           "fp8_block_quantize.hip", "fp8_block_gemm.hip", "moe_decode.hip"]
 CEILING_SOURCES = ["ceiling.hip"]
 LIB_CEILING = os.path.join(HERE, "libnvfp4_ceiling.so")
 

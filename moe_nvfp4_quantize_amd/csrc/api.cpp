@@ -92,6 +92,12 @@ nvfp4_status quantize_impl(const void *x, nvfp4_dtype x_type, int64_t rows, int6
   return from_hip(launch_quantize(p, x_type == NVFP4_BF16, vec, 1, rs, stream));
 }
 
+// shape rules of the few-token routed-expert layer (apart from its token limit)
+bool decode_shape_ok(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
+  return T >= 0 && E >= 1 && E <= 1024 && k >= 1 && k <= 32 && k <= E && H > 0 && H % 16 == 0 && I > 0 &&
+         I % 16 == 0 && H <= (1 << 20) && I <= (1 << 20);
+}
+
 // ---------------------------------------------- allocation-free quantize
 // Scratch of nvfp4_quantize_noalloc: the resident kernel's arrival state and
 // the amax partials (at most kMaxPartials per tensor, whatever its size).
@@ -312,6 +318,51 @@ nvfp4_status nvfp4_fp8_gemm(const uint8_t *a_q, const float *a_g, const uint8_t 
   return from_hip(launch_fp8_gemm(p, c_type == NVFP4_BF16 ? OutType::BF16 : OutType::F32, stream));
 }
 
+nvfp4_status nvfp4_fp8_block_quantize(const void *x, nvfp4_dtype x_type, int64_t rows, int64_t cols,
+                                      int64_t ld_x, int32_t block_rows, uint8_t *q, float *s,
+                                      hipStream_t stream) {
+  if (!valid_dtype(x_type) || !quant_shape_ok(rows, cols) || ld_x < cols) return NVFP4_ERR_INVALID_ARG;
+  if (block_rows != 1 && block_rows != 128) return NVFP4_ERR_INVALID_ARG;
+  if (rows == 0) return NVFP4_OK;
+  if (!x || !q || !s || !aligned16(q) || ((uintptr_t)s & 3u)) return NVFP4_ERR_INVALID_ARG;
+  if (((uintptr_t)x % dtype_size(x_type)) || ld_x > kI32Max * 64ll) return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status st = check_device();
+  if (st != NVFP4_OK) return st;
+  Fp8BlockQuantParams p{};
+  p.x = x;
+  p.ld = ld_x;
+  p.rows = (uint32_t)rows;
+  p.cols = (uint32_t)cols;
+  p.block_rows = (uint32_t)block_rows;
+  const uint32_t kb = (uint32_t)((cols + 127) / 128);
+  p.blocks = (uint32_t)((rows + block_rows - 1) / block_rows) * kb;
+  p.div_kb = FastDiv(kb);
+  p.q = q;
+  p.s = s;
+  const bool vec = aligned16(x) && (ld_x * (int64_t)dtype_size(x_type)) % 16 == 0;
+  return from_hip(launch_fp8_block_quantize(p, x_type == NVFP4_BF16, vec, stream));
+}
+
+nvfp4_status nvfp4_fp8_block_gemm(const uint8_t *a_q, const float *a_s, const uint8_t *b_q,
+                                  const float *b_s, int64_t M, int64_t N, int64_t K, void *c,
+                                  nvfp4_dtype c_type, int64_t ldc, hipStream_t stream) {
+  if (!valid_dtype(c_type) || M < 0 || N < 0 || K <= 0 || K % 16 != 0 || ldc < N)
+    return NVFP4_ERR_INVALID_ARG;
+  if (M > kI32Max || N > kI32Max || K > kI32Max) return NVFP4_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return NVFP4_OK;
+  if (!a_q || !a_s || !b_q || !b_s || !c || !aligned16(a_q) || !aligned16(b_q) || ((uintptr_t)a_s & 3u) ||
+      ((uintptr_t)b_s & 3u) || (uintptr_t)c % dtype_size(c_type))
+    return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status st = check_device();
+  if (st != NVFP4_OK) return st;
+  Fp8BlockGemmParams p{};
+  p.a_q = a_q; p.a_s = a_s;
+  p.b_q = b_q; p.b_s = b_s;
+  p.M = (uint32_t)M; p.N = (uint32_t)N; p.K = (uint32_t)K;
+  p.c = c; p.ldc = ldc;
+  return from_hip(launch_fp8_block_gemm(p, c_type == NVFP4_BF16 ? OutType::BF16 : OutType::F32, stream));
+}
+
 size_t nvfp4_moe_route_workspace_size(int64_t T, int32_t E, int32_t k) {
   if (T < 0 || E <= 0) return 0;
   return round_up(route_workspace_bytes(T, E, k), 256);
@@ -414,6 +465,44 @@ nvfp4_status nvfp4_moe_combine(const void *y, nvfp4_dtype y_type, const float *t
   if (st != NVFP4_OK) return st;
   return from_hip(launch_combine(y, y_type == NVFP4_BF16, topk_w, inv, T, k, H, out,
                                  out_type == NVFP4_BF16, stream));
+}
+
+size_t nvfp4_moe_decode_workspace_size(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
+  if (!decode_shape_ok(T, E, k, H, I) || T > (int64_t)kMaxDecodeTokens) return 0;
+  return moe_decode_workspace_bytes(T, E, k, H, I);
+}
+
+nvfp4_status nvfp4_moe_decode(const void *x, nvfp4_dtype x_type, int64_t ld_x, const float *logits,
+                              int64_t T, int32_t E, int32_t k, int64_t H, int64_t I,
+                              const uint8_t *gu_q, const uint8_t *gu_s, const float *gu_g,
+                              const uint8_t *d_q, const uint8_t *d_s, const float *d_g, void *out,
+                              nvfp4_dtype out_type, int64_t ld_out, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+  if (!valid_dtype(x_type) || !valid_dtype(out_type) || !decode_shape_ok(T, E, k, H, I) || ld_x < H ||
+      ld_out < H)
+    return NVFP4_ERR_INVALID_ARG;
+  if (T == 0) return NVFP4_OK;
+  if (!x || !logits || !gu_q || !gu_s || !gu_g || !d_q || !d_s || !d_g || !out) return NVFP4_ERR_INVALID_ARG;
+  if ((uintptr_t)x % dtype_size(x_type) || (uintptr_t)out % dtype_size(out_type) || ((uintptr_t)logits & 3u) ||
+      ((uintptr_t)gu_g & 3u) || ((uintptr_t)d_g & 3u))
+    return NVFP4_ERR_INVALID_ARG;
+  if (T > (int64_t)kMaxDecodeTokens) return NVFP4_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < moe_decode_workspace_bytes(T, E, k, H, I) || ((uintptr_t)workspace & 255u))
+    return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status st = check_device();
+  if (st != NVFP4_OK) return st;
+  MoeDecodeParams p{};
+  p.x = x; p.ld_x = ld_x; p.logits = logits;
+  p.T = (uint32_t)T; p.E = (uint32_t)E; p.k = (uint32_t)k; p.H = (uint32_t)H; p.I = (uint32_t)I;
+  p.gu_q = gu_q; p.gu_s = gu_s; p.gu_g = gu_g;
+  p.d_q = d_q; p.d_s = d_s; p.d_g = d_g;
+  p.out = out; p.ld_out = ld_out;
+  const bool x_vec = aligned16(x) && (ld_x * (int64_t)dtype_size(x_type)) % 16 == 0;
+  // 16-byte code loads and 4-byte scale loads: 64 elements of a row at a time
+  const bool gu_fast = H % 64 == 0 && aligned16(gu_q) && ((uintptr_t)gu_s & 3u) == 0;
+  const bool d_fast = I % 64 == 0 && aligned16(d_q) && ((uintptr_t)d_s & 3u) == 0;
+  return from_hip(launch_moe_decode(p, x_type == NVFP4_BF16, x_vec, gu_fast, d_fast, out_type == NVFP4_BF16,
+                                    workspace, stream));
 }
 
 }  // extern "C"

@@ -104,6 +104,32 @@ struct Fp8GemmParams {
 bool fp8_gemm_dma_ok(const Fp8GemmParams &p);
 hipError_t launch_fp8_gemm(const Fp8GemmParams &p, OutType out, hipStream_t stream);
 
+// ------------------------------------------------------- block-scaled FP8
+struct Fp8BlockQuantParams {
+  const void *x;
+  int64_t ld;  // row stride of x, elements
+  uint32_t rows, cols;
+  uint32_t block_rows;  // 1 or 128
+  uint32_t blocks;      // scales: ceil(rows / block_rows) * ceil(cols / 128)
+  FastDiv div_kb;       // by ceil(cols / 128)
+  uint8_t *q;           // [rows][cols]
+  float *s;             // [ceil(rows / block_rows)][ceil(cols / 128)]
+};
+
+hipError_t launch_fp8_block_quantize(const Fp8BlockQuantParams &p, bool bf16, bool vec, hipStream_t stream);
+
+struct Fp8BlockGemmParams {
+  const uint8_t *a_q;  // [M][K]
+  const float *a_s;    // [M][ceil(K / 128)]
+  const uint8_t *b_q;  // [N][K]
+  const float *b_s;    // [ceil(N / 128)][ceil(K / 128)]
+  uint32_t M, N, K;
+  void *c;
+  int64_t ldc;
+};
+
+hipError_t launch_fp8_block_gemm(const Fp8BlockGemmParams &p, OutType out, hipStream_t stream);
+
 // --------------------------------------------------------------------- MoE
 size_t route_workspace_bytes(int64_t T, int32_t E, int32_t k);
 hipError_t launch_route(const float *logits, int64_t T, int32_t E, int32_t k, int32_t *topk_ids,
@@ -111,5 +137,36 @@ hipError_t launch_route(const float *logits, int64_t T, int32_t E, int32_t k, in
                         void *workspace, hipStream_t stream);
 hipError_t launch_combine(const void *y, bool y_bf16, const float *w, const int32_t *inv, int64_t T,
                           int32_t k, int64_t H, void *out, bool out_bf16, hipStream_t stream);
+
+// The routed-expert layer for few tokens.  The caller fills the first part;
+// launch_moe_decode lays out the workspace and fills the rest.
+struct MoeDecodeParams {
+  const void *x;
+  int64_t ld_x;         // elements
+  const float *logits;  // [T][E]
+  uint32_t T, E, k, H, I;
+  const uint8_t *gu_q, *gu_s;  // [E][2I][H/2], [E][2I][H/16]
+  const float *gu_g;           // [E]
+  const uint8_t *d_q, *d_s;    // [E][H][I/2], [E][H][I/16]
+  const float *d_g;            // [E]
+  void *out;
+  int64_t ld_out;
+
+  uint32_t S, tiles_i;  // slots T k; 16-row tiles of I
+  int32_t *n_active;    // experts that some token picked
+  int4 *active;         // [E] (expert, first list entry, tokens)
+  int32_t *ids;         // [S] expert of slot t k + j
+  float *w;             // [S] routing weight
+  int32_t *list;        // [S] slots by expert, then token
+  uint16_t *xp;         // [3][T][H] bf16 planes of x
+  uint16_t *h;          // [3][S][I] bf16 planes of h
+  const uint16_t *xs;   // the rows the products read: x itself or xp
+  int64_t x_ld, x_plane;
+};
+
+constexpr uint32_t kMaxDecodeTokens = 128;
+size_t moe_decode_workspace_bytes(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I);
+hipError_t launch_moe_decode(MoeDecodeParams p, bool x_bf16, bool x_vec, bool gu_fast, bool d_fast, bool out_bf16,
+                             void *workspace, hipStream_t stream);
 
 }  // namespace nvfp4

@@ -18,6 +18,8 @@ import os
 
 import torch
 
+from .workloads import ceil_div
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnvfp4.so")
 
@@ -52,6 +54,9 @@ SIGNATURES = {
     "nvfp4_fp8_quantize": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_int, _P,
                                           _SZ, _P]),
     "nvfp4_fp8_gemm": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_int, _I64, _P]),
+    "nvfp4_fp8_block_quantize": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _I32, _P, _P, _P]),
+    "nvfp4_fp8_block_gemm": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_int, _I64,
+                                            _P]),
     "nvfp4_moe_route_workspace_size": (_SZ, [_I64, _I32, _I32]),
     "nvfp4_moe_route": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "nvfp4_moe_grouped_gemm": (ctypes.c_int, [_P, _P, _P, _I64, _P, _P, _I32, _I64, _P, _P, _P,
@@ -60,6 +65,9 @@ SIGNATURES = {
                                                          _P, _I64, _I64, _P, _P, _P, _P]),
     "nvfp4_moe_combine": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _I64, _I32, _I64, _I64, _P,
                                          ctypes.c_int, _P]),
+    "nvfp4_moe_decode_workspace_size": (_SZ, [_I64, _I32, _I32, _I64, _I64]),
+    "nvfp4_moe_decode": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _I64, _I32, _I32, _I64, _I64, _P, _P,
+                                        _P, _P, _P, _P, _P, ctypes.c_int, _I64, _P, _SZ, _P]),
 }
 
 _lib = None
@@ -126,6 +134,46 @@ def _on_gpu(*ts):
 
 def _ws(nbytes, device):
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+
+
+def _one_device(*ts):
+    """The GPU that every tensor is on."""
+    dev = ts[0].device
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("all tensors must be on the GPU")
+        if t.device != dev:
+            raise ValueError("all tensors must be on the same GPU")
+    return dev
+
+
+def _on_stream(device, stream, body):
+    """body(raw stream) with ``device`` current and ``stream`` (default: the
+    device's current one) as its current stream: what it allocates belongs to
+    the stream that its kernels run on."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return body(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            return body(torch.cuda.current_stream().cuda_stream)
+        if stream.device != device:
+            raise ValueError("stream and tensors are on different GPUs")
+        with torch.cuda.stream(stream):
+            return body(stream.cuda_stream)
+
+
+def _rows(t, rows, cols, what):
+    """Row stride of a 2-D tensor [rows, cols] whose rows are dense."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{what} must be [{rows}, {cols}]")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have unit stride along the last dim")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _dense(t, dtype, shape, what):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {dtype} of shape {tuple(shape)}")
 
 
 # nvfp4_quantize's workspace must start zero-filled and then be reused: one per
@@ -355,6 +403,67 @@ def nvfp4_fp8_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
     return out
 
 
+def nvfp4_fp8_block_quantize(x, block_rows=1, out=None, stream=None):
+    """Block-scaled FP8 quantize of a 2-D f32/bf16 GPU tensor -> (q uint8 [rows, cols],
+    s float32 [ceil(rows / block_rows), ceil(cols / 128)]).
+
+    ``block_rows`` 1 (a scale per row and 128 columns: activations) or 128 (a scale per
+    128 x 128 tile: weights).  ``out``: optional preallocated (q, s)."""
+    lib = load_library()
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    rows, cols = x.shape
+    ld = _rows(x, rows, cols, "x")
+    code = _dtype_code(x.dtype)
+    s_shape = (ceil_div(rows, block_rows), ceil_div(cols, 128))
+    if out is not None:
+        _dense(out[0], torch.uint8, (rows, cols), "q")
+        _dense(out[1], torch.float32, s_shape, "s")
+    dev = _one_device(x, *(out or ()))
+
+    def body(hs):
+        q, s = out if out is not None else (torch.empty((rows, cols), dtype=torch.uint8, device=dev),
+                                            torch.empty(s_shape, dtype=torch.float32, device=dev))
+        st = lib.nvfp4_fp8_block_quantize(x.data_ptr(), code, rows, cols, ld, block_rows, q.data_ptr(),
+                                          s.data_ptr(), hs)
+        _check("nvfp4_fp8_block_quantize", st)
+        return q, s
+
+    return _on_stream(dev, stream, body)
+
+
+def nvfp4_fp8_block_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
+    """C = A_hat @ B_hat^T for block-scaled FP8 tensors: a = (q [M, K], s [M, ceil(K/128)])
+    with a scale per row and 128 columns, b = (q [N, K], s [ceil(N/128), ceil(K/128)]) with
+    a scale per 128 x 128 tile."""
+    lib = load_library()
+    a_q, a_s = a
+    b_q, b_s = b
+    if a_q.dim() != 2 or b_q.dim() != 2 or a_q.shape[1] != b_q.shape[1]:
+        raise ValueError("K mismatch between A and B")
+    M, K = a_q.shape
+    N = b_q.shape[0]
+    kb = ceil_div(K, 128)
+    _dense(a_q, torch.uint8, (M, K), "a's q")
+    _dense(a_s, torch.float32, (M, kb), "a's s")
+    _dense(b_q, torch.uint8, (N, K), "b's q")
+    _dense(b_s, torch.float32, (ceil_div(N, 128), kb), "b's s")
+    ldc = N if out is None else _rows(out, M, N, "out")
+    code = _dtype_code(out_dtype if out is None else out.dtype)
+    dev = _one_device(a_q, a_s, b_q, b_s, *(() if out is None else (out,)))
+
+    def body(hs):
+        c = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
+        st = lib.nvfp4_fp8_block_gemm(a_q.data_ptr(), a_s.data_ptr(), b_q.data_ptr(), b_s.data_ptr(), M, N, K,
+                                      c.data_ptr(), code, ldc, hs)
+        _check("nvfp4_fp8_block_gemm", st)
+        return c
+
+    return _on_stream(dev, stream, body)
+
+
 # ----------------------------------------------------------------------- MoE
 
 
@@ -458,3 +567,41 @@ def moe_layer(x, logits, k, w_gate_up, w_down, stream=None, keep=False, inter_dt
     if keep:
         return dict(r, xq=xq, h=h, hq=hq, y=y, out=out)
     return out
+
+
+def nvfp4_moe_decode(x, logits, k, w_gate_up, w_down, out_dtype=torch.bfloat16, out=None, stream=None):
+    """The whole routed-expert layer for few tokens (at most 128), activations not quantized.
+
+    x bf16/f32 [T, H]; logits float32 [T, E]; w_gate_up and w_down quantized expert stacks
+    (q, s, g) for [E, 2I, H] and [E, H, I], as for :func:`moe_layer`."""
+    lib = load_library()
+    gu_q, gu_s, gu_g = w_gate_up
+    d_q, d_s, d_g = w_down
+    if x.dim() != 2 or logits.dim() != 2 or gu_q.dim() != 3 or d_q.dim() != 3:
+        raise ValueError("x and logits must be 2-D, the weights' q 3-D")
+    T, H = x.shape
+    E, I = logits.shape[1], d_q.shape[2] * 2
+    if H % 16 != 0 or I % 16 != 0:
+        raise ValueError("H and I must be multiples of 16")
+    ld_x = _rows(x, T, H, "x")
+    _dense(logits, torch.float32, (T, E), "logits")
+    _dense(gu_q, torch.uint8, (E, 2 * I, H // 2), "w_gate_up's q")
+    _dense(gu_s, torch.uint8, (E, 2 * I, H // 16), "w_gate_up's s")
+    _dense(gu_g, torch.float32, (E,), "w_gate_up's g")
+    _dense(d_q, torch.uint8, (E, H, I // 2), "w_down's q")
+    _dense(d_s, torch.uint8, (E, H, I // 16), "w_down's s")
+    _dense(d_g, torch.float32, (E,), "w_down's g")
+    ld_out = H if out is None else _rows(out, T, H, "out")
+    dev = _one_device(x, logits, gu_q, gu_s, gu_g, d_q, d_s, d_g, *(() if out is None else (out,)))
+    x_code, o_code = _dtype_code(x.dtype), _dtype_code(out_dtype if out is None else out.dtype)
+
+    def body(hs):
+        o = torch.empty((T, H), dtype=out_dtype, device=dev) if out is None else out
+        ws = _ws(lib.nvfp4_moe_decode_workspace_size(T, E, k, H, I), dev)
+        st = lib.nvfp4_moe_decode(x.data_ptr(), x_code, ld_x, logits.data_ptr(), T, E, k, H, I, gu_q.data_ptr(),
+                                  gu_s.data_ptr(), gu_g.data_ptr(), d_q.data_ptr(), d_s.data_ptr(),
+                                  d_g.data_ptr(), o.data_ptr(), o_code, ld_out, ws.data_ptr(), ws.numel(), hs)
+        _check("nvfp4_moe_decode", st)
+        return o
+
+    return _on_stream(dev, stream, body)

@@ -1,0 +1,196 @@
+"""GPU parity of the block-scaled FP8 quantize and GEMM against their oracle.
+
+Quantized bytes and scales are bit-exact.  GEMM outputs lie within the oracle's bound on a
+float32 evaluation, element by element; a bf16 output half a bf16 step (2^-8 relative at
+most) further.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8_block as P
+from moe_nvfp4_quantize_amd import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from moe_nvfp4_quantize_amd import nvfp4
+    nvfp4.load_library()
+    return nvfp4
+
+
+def _host(t):
+    return t.detach().float().cpu().numpy()
+
+
+def _same(got, want, label):
+    np.testing.assert_array_equal(got[1].cpu().numpy(), want[1], err_msg=str(label))
+    np.testing.assert_array_equal(got[0].cpu().numpy(), want[0], err_msg=str(label))
+
+
+def _uneven(rows, cols, seed, dtype):
+    x = W.random_matrix(rows, cols, seed=seed, device="cuda") * torch.exp(
+        2 * W.random_matrix(1, cols, seed=seed + 1, device="cuda"))
+    return x.to(dtype)
+
+
+# ------------------------------------------------------------------ quantize
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 5120), (3, 128), (127, 272), (128, 256), (129, 2064), (300, 144)])
+def test_quantize_bit_exact(B, rows, cols, dtype, block_rows):
+    x = _uneven(rows, cols, rows + cols, dtype)
+    _same(B.nvfp4_fp8_block_quantize(x, block_rows), P.quantize(_host(x), block_rows), (rows, cols))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_midpoints(B, dtype):
+    """Values that sit on midpoints of two codes of the real scale or one unit beside them, for
+    block maxima whose scale is no float32; subnormal codes; signed zeros."""
+    rng = np.random.default_rng(11)
+    from oracle.formats import e4m3_decode
+    mids = (e4m3_decode(np.arange(126)) + e4m3_decode(np.arange(1, 127))) / 2
+    rows = []
+    for amax in (1.0, 0.75, 1.5, 3.0, 5.5, 1e-3, 448.0, 447.0, 2.0 ** -70, 1.3 * 2.0 ** -118, 2.0 ** -130, 3e38):
+        s = float(max(np.float32(amax) / np.float32(448.0), np.float32(2.0 ** -126)))
+        near = np.float32(mids * s)
+        for v in (near, np.nextafter(near, np.float32(0)), np.nextafter(near, np.float32(np.inf)),
+                  np.float32(mids * (amax / 448.0))):
+            row = np.zeros(128, np.float32)
+            row[:126] = np.minimum(v, np.float32(amax)) * rng.choice([-1, 1], 126)
+            row[126], row[127] = amax, -0.0
+            rows.append(row)
+    x = torch.from_numpy(np.stack(rows)).cuda().to(dtype)
+    for br in (1, 128):
+        _same(B.nvfp4_fp8_block_quantize(x, br), P.quantize(_host(x), br), br)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_strides_alignment_out(B, dtype):
+    big = _uneven(140, 700, 5, dtype)
+    for x in (big[:, :272], big[:, 3:275], big[::2, 1:401]):
+        for br in (1, 128):
+            q = torch.empty(x.shape, dtype=torch.uint8, device="cuda")
+            s = torch.empty((-(-x.shape[0] // br), -(-x.shape[1] // 128)), device="cuda")
+            got = B.nvfp4_fp8_block_quantize(x, br, out=(q, s))
+            assert got[0] is q and got[1] is s
+            _same(got, P.quantize(_host(x), br), br)
+    zero = torch.zeros((130, 144), dtype=dtype, device="cuda")
+    q, s = B.nvfp4_fp8_block_quantize(zero, 128)
+    assert torch.all(q == 0) and torch.all(s == 1)
+    q, s = B.nvfp4_fp8_block_quantize(zero[:0])
+    assert q.shape == (0, 144) and s.shape == (0, 2)
+
+
+# ---------------------------------------------------------------------- GEMM
+
+
+def _operands(M, N, K, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+
+    def codes(rows):
+        return (torch.randn((rows, K), generator=g, device="cuda") * 120).clamp(-448, 448) \
+            .to(torch.float8_e4m3fn).view(torch.uint8)
+
+    def scales(rows):
+        return torch.exp(torch.randn((rows, -(-K // 128)), generator=g, device="cuda")) * 0.01
+
+    return (codes(M), scales(M)), (codes(N), scales(-(-N // 128)))
+
+
+def _check(B, M, N, K, dtype, out=None, a=None, b=None, seed=0):
+    a0, b0 = _operands(M, N, K, seed + M + N + K)
+    a, b = a or a0, b or b0
+    y = B.nvfp4_fp8_block_gemm(a, b, out_dtype=dtype, out=out)
+    args = [t.cpu().numpy() for t in (*a, *b)]
+    ref, tol = P.gemm(*args), P.gemm_bound(*args)
+    if dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    err = np.abs(y.double().cpu().numpy() - ref)
+    worst = np.max(err / np.maximum(tol, 1e-300))
+    rel = np.linalg.norm(err) / max(np.linalg.norm(ref), 1e-300)
+    print(f"[fp8 block gemm] {M}x{N}x{K} {dtype}: {worst:.3f} of the bound, rel {rel:.2e}", flush=True)
+    assert worst <= 1.0, (M, N, K, worst)
+    return y
+
+
+SHAPES = [(1, 1, 16), (1, 512, 512), (2, 17, 144), (7, 130, 272), (16, 256, 5120), (17, 300, 1040), (33, 129, 128),
+          (64, 640, 2048), (65, 1000, 640), (100, 96, 8192), (128, 384, 1024), (129, 257, 2064), (255, 520, 384),
+          (256, 512, 1280), (300, 770, 1552), (513, 1030, 256)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_gemm(B, M, N, K, dtype):
+    _check(B, M, N, K, dtype)
+
+
+@pytest.mark.parametrize("M", [1, 5, 40, 200])
+def test_gemm_output_strides(B, M):
+    """Rows of a wider buffer, at element alignment; what lies beside them stays."""
+    N, K = 200, 384
+    for dtype in (torch.bfloat16, torch.float32):
+        for first, wide in ((0, 256), (1, 203), (3, 301)):
+            buf = torch.full((M, wide + first), 7.0, dtype=dtype, device="cuda")
+            _check(B, M, N, K, dtype, out=buf[:, first:first + N])
+            assert torch.all(buf[:, :first] == 7) and torch.all(buf[:, first + N:] == 7)
+
+
+@pytest.mark.parametrize("M", [3, 70, 260])
+def test_gemm_zero_scales_and_codes(B, M):
+    a, b = _operands(M, 260, 400, 9)
+    a[1][:, 1] = 0
+    a[0][M // 2] = 0
+    b[1][1] = 0
+    y = _check(B, M, 260, 400, torch.float32, a=a, b=b)
+    assert torch.all(y[M // 2] == 0) and torch.all(y[:, 128:256] == 0)
+    assert B.nvfp4_fp8_block_gemm((a[0][:0], a[1][:0]), b).shape == (0, 260)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 200, 5120), (32, 640, 2064), (90, 300, 1024), (300, 600, 1024)])
+def test_gemm_same_bits_every_time(B, M, N, K):
+    a, b = _operands(M, N, K, 1)
+    y = B.nvfp4_fp8_block_gemm(a, b, out_dtype=torch.float32)
+    for _ in range(3):
+        assert torch.equal(y, B.nvfp4_fp8_block_gemm(a, b, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("M", [1, 48, 150])
+def test_quantize_then_gemm_graph_and_stream(B, M):
+    """The two as a linear layer, on a side stream and captured: replays on rewritten inputs with
+    eager work between equal the eager result."""
+    K, N = 1280, 390
+    w = B.nvfp4_fp8_block_quantize(_uneven(N, K, 4, torch.bfloat16), 128)
+    x = _uneven(M, K, 6, torch.bfloat16)
+    q = torch.empty((M, K), dtype=torch.uint8, device="cuda")
+    s = torch.empty((M, K // 128), device="cuda")
+    y = torch.empty((M, N), device="cuda")
+
+    def layer(stream=None):
+        B.nvfp4_fp8_block_quantize(x, out=(q, s), stream=stream)
+        return B.nvfp4_fp8_block_gemm((q, s), w, out=y, stream=stream)
+
+    want = layer().clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    layer(side)
+    side.synchronize()
+    assert torch.equal(y, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer()
+    for i in range(3):
+        x.copy_(_uneven(M, K, 60 + i, torch.bfloat16))
+        want = layer().clone()
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), i
