@@ -138,10 +138,379 @@ __global__ __launch_bounds__(256) void block_gemm_plain_kernel(Fp8BlockGemmParam
   }
 }
 
+// Few rows (M <= 16 MT): bound by one read of B.  A workgroup owns 16 NR columns
+// of C and its NW waves take the 128-column blocks of K in turn, U blocks' loads
+// in flight together; a weight fragment is used for all MT row tiles.  The waves'
+// sums are joined through LDS in wave order.
+template <int MT, int NR, int NW, int U, typename OutT>
+__global__ __launch_bounds__(NW * 64) void block_gemm_skinny_kernel(Fp8BlockGemmParams p) {
+  __shared__ __attribute__((aligned(16))) float red[NW][MT * 16][NR * 16 + 4];
+  const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64;
+  const uint32_t l16 = lane % 16, lq = lane / 16;
+  const uint32_t n0 = blockIdx.x * (16 * NR);
+  const uint64_t K = p.K;
+  const uint32_t KB = (p.K + 127) / 128;
+  const uint8_t *br[NR], *ar[MT];
+  const float *as[MT];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) br[i] = p.b_q + (uint64_t)min(n0 + 16 * i + l16, p.N - 1) * K;
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const uint64_t m = min(16 * j + l16, p.M - 1);
+    ar[j] = p.a_q + m * K;
+    as[j] = p.a_s + m * KB;
+  }
+  const float *bs = p.b_s + (uint64_t)(n0 / 128) * KB;  // 16 NR columns lie in one scale row
+  float4v acc[NR][MT];
+#pragma unroll
+  for (int i = 0; i < NR; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = (float4v){0, 0, 0, 0};
+  for (uint32_t kb0 = wave; kb0 < KB; kb0 += NW * U) {
+    Fp8Frag fb[U][NR], fa[U][MT];
+    float f[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t kb = kb0 + NW * u;
+      const uint64_t k = (uint64_t)kb * 128 + 32 * lq;
+#pragma unroll
+      for (int i = 0; i < NR; ++i) fb[u][i] = load_frag(br[i], k, K);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        fa[u][j] = load_frag(ar[j], k, K);
+        f[u][j] = kb < KB ? as[j][kb] * bs[kb] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const float4v part = mul16<kExact<OutT>>(fb[u][i], fa[u][j], (float4v){0, 0, 0, 0});
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(part[r], f[u][j], acc[i][j][r]);
+        }
+  }
+  // accumulator r of lane (l16, lq): row 16 j + l16, column 16 i + 4 lq + r
+#pragma unroll
+  for (int i = 0; i < NR; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) *reinterpret_cast<float4v *>(&red[wave][16 * j + l16][16 * i + 4 * lq]) = acc[i][j];
+  __syncthreads();
+  OutT *Cp = static_cast<OutT *>(p.c);
+  for (uint32_t c = tid; c < p.M * (16 * NR); c += NW * 64) {
+    const uint32_t m = c / (16 * NR), n = c % (16 * NR);
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v += red[w][m][n];
+    if (n0 + n < p.N) Cp[(int64_t)m * p.ldc + n0 + n] = to_out<OutT>(v);
+  }
+}
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float float2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+
+// Swizzle of the eight 16-byte pieces of a 128-byte LDS row: piece c of row r is
+// stored at c ^ swz128(r).  A 16-byte read is served 16 lanes at a time, which in
+// the fragment reads are 16 consecutive rows at one piece: r % 2 gives the half
+// of a 256-byte window and swz128 a different piece of it for every two rows.
+__device__ __forceinline__ uint32_t swz128(uint32_t r) { return (r >> 1) & 7u; }
+
+// Many rows: a BM x BN tile per workgroup, NWM x NWN waves of 64 x WN each.
+//  * One step is one 128-column block: its tiles of A and B (128 bytes a row) and
+//    A's scales go from global memory straight into LDS (buffer loads, 1 KB a
+//    transfer), NST stages, fetched NST steps ahead.  The resources end at the
+//    matrix's last row, so rows past it read nothing and need no clamp.
+//  * Fragments are double buffered in registers: those of step s + 1 are read
+//    from LDS behind the matrix instructions of step s.  They may live in the
+//    accumulation half of the register file (matrix instructions and LDS reads
+//    reach it), while the sums, which the vector unit adds to, live in the other
+//    (this file is compiled with -amdgpu-mfma-vgpr-form for that).
+//  * The float32 join costs one FMA per output and block on the vector unit
+//    beside two matrix instructions per 32 x 32 outputs: the FMAs of one column
+//    fragment run under the matrix instructions of the next.
+//  * The weight fragment goes first, so a lane's accumulators are runs of four
+//    columns of one row: its scale is one factor, and the epilogue stages 8- or
+//    16-byte pieces through LDS and stores 16 bytes a lane.
+//  * K % 128 != 0: the last block's pieces past K are zeroed as they are read
+//    (their transfers are pointed at the row's first piece).
+template <int BM, int BN, int NWM, int NWN, int NST, bool VSTORE, typename OutT>
+__global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8BlockGemmParams p) {
+  constexpr int NW = NWM * NWN, WM = BM / NWM, WN = BN / NWN, FM = WM / 32, FN = WN / 32;
+  static_assert(WM == 64, "a wave's 64 row scales are one transfer");
+  static_assert(128 % WN == 0, "a wave's columns lie in one scale row");
+  constexpr int TA = BM / 8 / NW, TB = BN / 8 / NW;  // transfers of 8 rows per wave and step
+  constexpr int TN = TA + TB + 1;
+  constexpr int OFF_B = BM * 128, OFF_S = OFF_B + BN * 128, STAGE = OFF_S + NW * 256;
+  constexpr bool EXACT = kExact<OutT>;
+  static_assert(NST * STAGE <= 160 * 1024, "LDS");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NST * STAGE];
+
+  const uint32_t tid = threadIdx.x;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64;
+  const uint32_t K = p.K, KB = (K + 127) / 128;
+  const uint32_t tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
+  uint32_t tm, tn;
+  dense_tile(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
+  const uint32_t row0 = tm * BM, col0 = tn * BN;
+  const uint32_t wm = wave / NWN, wn = wave % NWN;
+
+  typedef __amdgpu_buffer_rsrc_t Rsrc;
+  auto rsrc = [](const void *base, uint32_t bytes) -> Rsrc {
+    return __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, (int)bytes, 0x00020000);
+  };
+  const uint32_t rows_a = min(p.M - row0, (uint32_t)BM), rows_b = min(p.N - col0, (uint32_t)BN);
+  const Rsrc rA = rsrc(p.a_q + (size_t)row0 * K, rows_a * K);
+  const Rsrc rB = rsrc(p.b_q + (size_t)col0 * K, rows_b * K);
+  const Rsrc rS = rsrc(p.a_s + (size_t)row0 * KB, rows_a * KB * 4);
+  // transfer j of an operand: tile rows (j NW + wave) * 8 + lane / 8, physical
+  // piece lane % 8 (the swizzle repeats every 16 rows: the same for every j when
+  // 8 NW is a multiple of 16)
+  static_assert(NW % 2 == 0, "swizzle phase");
+  const uint32_t trow = wave * 8 + lane / 8;
+  const uint32_t piece = ((lane % 8) ^ swz128(trow)) * 16;
+  const uint32_t first = trow * K;
+  const uint32_t srow = (wm * 64 + lane) * KB * 4;
+  // the transfers of block kb into stage buf; q-th of TN
+  auto issue = [&](uint32_t buf, uint32_t kb, int q) {
+    uint8_t *st = smem + buf * STAGE;
+    const uint32_t v = first + (kb * 128 + piece < K ? piece : 0u);
+    const int so = (int)(kb * 128);
+    if (q < TA)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(st + (q * NW + wave) * 1024), 16,
+                                               (int)(v + q * (NW * 8) * K), so, 0, 0);
+    else if (q < TA + TB)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(st + OFF_B + ((q - TA) * NW + wave) * 1024), 16,
+                                               (int)(v + (q - TA) * (NW * 8) * K), so, 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rS, (lds_void *)(st + OFF_S + wave * 256), 4, (int)srow, (int)(kb * 4),
+                                               0, 0);
+  };
+
+  const uint32_t l32 = lane % 32, lh = lane / 32;
+  struct Frags {
+    Fp8Frag a[FM][2], b[FN][2];
+    float s[FM];
+    float sb;
+  };
+  // pieces 4t + 2 lh + h (t: half of the block) of fragment rows; row groups of
+  // 32 share a swizzle phase
+  uint32_t oa[2][2], ob[2][2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t c = ((4 * t + 2 * lh + h) ^ swz128(l32)) * 16;
+      oa[t][h] = (wm * WM + l32) * 128 + c;
+      ob[t][h] = OFF_B + (wn * WN + l32) * 128 + c;
+    }
+  const float *bs = p.b_s + (size_t)(min(col0 + wn * WN, p.N - 1) / 128) * KB;
+  auto read = [&](uint32_t buf, uint32_t kb, Frags &x) {
+    const uint8_t *st = smem + buf * STAGE;
+    x.sb = bs[kb];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        x.a[i][t].lo = *reinterpret_cast<const u32x4 *>(st + oa[t][0] + i * 4096);
+        x.a[i][t].hi = *reinterpret_cast<const u32x4 *>(st + oa[t][1] + i * 4096);
+      }
+      x.s[i] = *reinterpret_cast<const float *>(st + OFF_S + wave * 256 + (i * 32 + l32) * 4);
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        x.b[j][t].lo = *reinterpret_cast<const u32x4 *>(st + ob[t][0] + j * 4096);
+        x.b[j][t].hi = *reinterpret_cast<const u32x4 *>(st + ob[t][1] + j * 4096);
+      }
+  };
+  // pieces past the last `left` bytes of a block
+  auto cut = [&](Frags &x, uint32_t left) {
+    auto one = [&](Fp8Frag &f, int t) {
+      const uint32_t c = (4 * t + 2 * lh) * 16;
+      if (c >= left) f.lo = (u32x4){0, 0, 0, 0};
+      if (c + 16 >= left) f.hi = (u32x4){0, 0, 0, 0};
+    };
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) one(x.a[i][t], t);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) one(x.b[j][t], t);
+    }
+  };
+
+  float16v acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  auto multiply = [&](const Frags &x) {
+    float f[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) f[i] = x.s[i] * x.sb;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      float16v part[FM];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) part[i] = mul32<EXACT>(x.b[j][0], x.a[i][0], (float16v){});
+#pragma unroll
+      for (int i = 0; i < FM; ++i) part[i] = mul32<EXACT>(x.b[j][1], x.a[i][1], part[i]);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(part[i][r], f[i], acc[i][j][r]);
+    }
+  };
+
+  // Step s: its fragments are in registers; stage s + 1 has landed (own
+  // transfers waited for, then the barrier for everyone's), and buffer s % NST is
+  // free (its reads were waited for before the barrier): it takes block s + NST.
+  // Past the end the last block is fetched again, into a stage nobody reads, so
+  // that one wait count serves every step.
+#pragma unroll
+  for (int st = 0; st < NST; ++st)
+#pragma unroll
+    for (int q = 0; q < TN; ++q) issue(st, min((uint32_t)st, KB - 1), q);
+  wait_vm<(NST - 1) * TN>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  Frags x[2];
+  read(0, 0, x[0]);
+  uint32_t cur = 0;  // s % NST
+  auto step = [&](uint32_t s, auto tag) {
+    constexpr int C = decltype(tag)::value;
+    wait_vm<(NST - 2) * TN>();
+    wait_lgkm0();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const uint32_t nxt = cur + 1 == NST ? 0 : cur + 1;
+    read(nxt, min(s + 1, KB - 1), x[C ^ 1]);
+    const uint32_t kb = min(s + NST, KB - 1);
+#pragma unroll
+    for (int q = 0; q < TN; ++q) issue(cur, kb, q);
+    multiply(x[C]);
+    cur = nxt;
+  };
+  uint32_t s = 0;
+  const uint32_t whole = K / 128;
+  for (; s + 2 <= whole; s += 2) {
+    step(s, std::integral_constant<int, 0>());
+    step(s + 1, std::integral_constant<int, 1>());
+  }
+  wait_lgkm0();
+  if (s < whole) {  // one more whole block
+    step(s, std::integral_constant<int, 0>());
+    wait_lgkm0();
+    if (s + 1 < KB) {
+      cut(x[1], K - whole * 128);
+      multiply(x[1]);
+    }
+  } else if (s < KB) {
+    cut(x[0], K - whole * 128);
+    multiply(x[0]);
+  }
+  // every transfer has landed and every wave is past its last read: all of LDS
+  // is free for the epilogue
+  wait_vm<0>();
+  wait_lgkm0();
+  __syncthreads();
+
+  // ---------------------------------------------------------------- epilogue
+  // Accumulator 4q + e of lane (l32, lh): row l32, column 8q + 4 lh + e of the
+  // fragment.  Each wave stages 32 rows x WN columns at a time in its own part of
+  // LDS, 16-byte chunks of row t rotated by t / (rows per 256 bytes), then reads
+  // every chunk back and writes it out 16 bytes a lane.
+  constexpr int ROW_BYTES = WN * (int)sizeof(OutT);
+  constexpr int CPR = ROW_BYTES / 16;
+  constexpr int RW = ROW_BYTES >= 256 ? 1 : 256 / ROW_BYTES;
+  static_assert(NW * 32 * ROW_BYTES <= NST * STAGE, "epilogue staging must fit");
+  uint8_t *slab = smem + wave * 32 * ROW_BYTES;
+  auto at = [&](uint32_t t, uint32_t c) { return t * ROW_BYTES + ((c + t / RW) % CPR) * 16; };
+  OutT *Cp = static_cast<OutT *>(p.c);
+  const uint32_t ccol0 = col0 + wn * WN;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v0 = acc[i][j][4 * q], v1 = acc[i][j][4 * q + 1];
+        const float v2 = acc[i][j][4 * q + 2], v3 = acc[i][j][4 * q + 3];
+        if constexpr (sizeof(OutT) == 2) {
+          const float2v f01 = {v0, v1}, f23 = {v2, v3};
+          const u32x2 pk = {__builtin_bit_cast(uint32_t, __builtin_convertvector(f01, bf16x2v)),
+                            __builtin_bit_cast(uint32_t, __builtin_convertvector(f23, bf16x2v))};
+          *reinterpret_cast<u32x2 *>(slab + at(l32, 4 * j + q) + lh * 8) = pk;
+        } else {
+          const u32x4 fv = {f2u(v0), f2u(v1), f2u(v2), f2u(v3)};
+          *reinterpret_cast<u32x4 *>(slab + at(l32, 8 * j + 2 * q + lh)) = fv;
+        }
+      }
+    }
+    // the slab is this wave's own: ordering inside the wave suffices
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    constexpr int VEC = 16 / (int)sizeof(OutT);
+    constexpr int NIT = 32 * CPR / 64;
+    const uint32_t rbase = row0 + wm * WM + i * 32;
+    u32x4 chunk[NIT];
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+      const uint32_t c = lane + it * 64;
+      chunk[it] = *reinterpret_cast<const u32x4 *>(slab + at(c / CPR, c % CPR));
+    }
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+      const uint32_t c = lane + it * 64;
+      const uint32_t row = rbase + c / CPR, col = ccol0 + (c % CPR) * VEC;
+      if (row >= p.M) continue;
+      OutT *gp = Cp + (int64_t)row * p.ldc + col;
+      if (VSTORE && col + VEC <= p.N) {
+        *reinterpret_cast<u32x4 *>(gp) = chunk[it];
+      } else {
+        OutT sv[VEC];
+        __builtin_memcpy(sv, &chunk[it], 16);
+        for (int e = 0; e < VEC; ++e)
+          if (col + e < p.N) gp[e] = sv[e];
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <int MT, int NR, int NW, int U, typename OutT>
+hipError_t launch_skinny(const Fp8BlockGemmParams &p, hipStream_t stream) {
+  block_gemm_skinny_kernel<MT, NR, NW, U, OutT><<<(p.N + 16 * NR - 1) / (16 * NR), NW * 64, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <int BM, int BN, int NWM, int NWN, int NST, typename OutT>
+hipError_t launch_tile(const Fp8BlockGemmParams &p, hipStream_t stream) {
+  const bool vstore = ((uintptr_t)p.c % 16 == 0) && (p.ldc * (int64_t)sizeof(OutT)) % 16 == 0;
+  const uint32_t grid = ((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
+  if (vstore) block_gemm_tile_kernel<BM, BN, NWM, NWN, NST, true, OutT><<<grid, NWM * NWN * 64, 0, stream>>>(p);
+  else block_gemm_tile_kernel<BM, BN, NWM, NWN, NST, false, OutT><<<grid, NWM * NWN * 64, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
 template <typename OutT>
 hipError_t launch_typed(const Fp8BlockGemmParams &p, hipStream_t stream) {
+  if (p.M <= 16) return launch_skinny<1, 1, 8, 4, OutT>(p, stream);
+  if (p.M <= 32) return launch_skinny<2, 2, 8, 2, OutT>(p, stream);
+  if (p.M <= 64) return launch_skinny<4, 2, 8, 1, OutT>(p, stream);
+  // the tile kernel's resources hold 256 rows: 32-bit offsets
+  if ((uint64_t)p.K * 256 < (1ull << 32)) {
+    if (p.M <= 128) return launch_tile<128, 128, 2, 2, 4, OutT>(p, stream);
+    return launch_tile<128, 256, 2, 2, 3, OutT>(p, stream);
+  }
   const uint64_t grid = (uint64_t)((p.M + 63) / 64) * ((p.N + 63) / 64);
-  if (grid > 0x7FFFFFFFull) return hipErrorInvalidValue;
   block_gemm_plain_kernel<OutT><<<(uint32_t)grid, 256, 0, stream>>>(p);
   return hipGetLastError();
 }
