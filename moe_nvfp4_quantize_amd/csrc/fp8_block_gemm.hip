@@ -306,26 +306,25 @@ __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8Bl
       oa[t][h] = (wm * WM + l32) * 128 + c;
       ob[t][h] = OFF_B + (wn * WN + l32) * 128 + c;
     }
-  const float *bs = p.b_s + (size_t)(min(col0 + wn * WN, p.N - 1) / 128) * KB;
-  auto read = [&](uint32_t buf, uint32_t kb, Frags &x) {
-    const uint8_t *st = smem + buf * STAGE;
-    x.sb = bs[kb];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        x.a[i][t].lo = *reinterpret_cast<const u32x4 *>(st + oa[t][0] + i * 4096);
-        x.a[i][t].hi = *reinterpret_cast<const u32x4 *>(st + oa[t][1] + i * 4096);
-      }
-      x.s[i] = *reinterpret_cast<const float *>(st + OFF_S + wave * 256 + (i * 32 + l32) * 4);
+  // B's scales are uniform over a wave: scalar loads (constant address space),
+  // outside the vector loads' count
+  typedef const float __attribute__((address_space(4))) cfloat;
+  cfloat *bs = (cfloat *)(uintptr_t)(p.b_s + (size_t)(min(col0 + wn * WN, p.N - 1) / 128) * KB);
+  // the d-th of ND reads of a stage (at byte st of LDS) into x
+  constexpr int ND = 5 * FM + 4 * FN;
+  auto read = [&](uint32_t st, Frags &x, int d) {
+    if (d < FM) {
+      x.s[d] = *reinterpret_cast<const float *>(smem + st + OFF_S + wave * 256 + (d * 32 + l32) * 4);
+      return;
     }
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        x.b[j][t].lo = *reinterpret_cast<const u32x4 *>(st + ob[t][0] + j * 4096);
-        x.b[j][t].hi = *reinterpret_cast<const u32x4 *>(st + ob[t][1] + j * 4096);
-      }
+    d -= FM;
+    const bool isA = d < 4 * FM;
+    if (!isA) d -= 4 * FM;
+    const int g = d / 4, t = d / 2 % 2, h = d % 2;
+    Fp8Frag &f = isA ? x.a[g][t] : x.b[g][t];
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(smem + st + (isA ? oa[t][h] : ob[t][h]) + g * 4096);
+    if (h == 0) f.lo = v;
+    else f.hi = v;
   };
   // pieces past the last `left` bytes of a block
   auto cut = [&](Frags &x, uint32_t left) {
@@ -351,21 +350,33 @@ __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8Bl
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  auto multiply = [&](const Frags &x) {
-    float f[FM];
+  // Unit u = (column fragment u / FM, row fragment u % FM) of a block: two matrix
+  // instructions.  Its FMAs run under the next unit's (the last unit's under the
+  // next block's first), so they never wait for a result.
+  constexpr int NU = FM * FN;
+  float16v part[2];
+  float pf = 0.0f;  // factor of the unit whose FMAs are due
+  auto join_unit = [&](int u, const float16v &v, float f, int from, int to) {
+    const int i = u % FM, j = u / FM;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) f[i] = x.s[i] * x.sb;
+    for (int r = from; r < to; ++r) acc[i][j][r] = __builtin_fmaf(v[r], f, acc[i][j][r]);
+  };
+  // under(u) runs behind unit u's first matrix instruction
+  auto multiply = [&](const Frags &x, auto under) {
+    static_assert(NU % 2 == 0, "the part buffers alternate over units and blocks");
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      float16v part[FM];
-#pragma unroll
-      for (int i = 0; i < FM; ++i) part[i] = mul32<EXACT>(x.b[j][0], x.a[i][0], (float16v){});
-#pragma unroll
-      for (int i = 0; i < FM; ++i) part[i] = mul32<EXACT>(x.b[j][1], x.a[i][1], part[i]);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(part[i][r], f[i], acc[i][j][r]);
+    for (int u = 0; u < NU; ++u) {
+      const int i = u % FM, j = u / FM;
+      part[u % 2] = mul32<EXACT>(x.b[j][0], x.a[i][0], (float16v){});
+      __builtin_amdgcn_sched_barrier(0);
+      under(u);
+      join_unit((u + NU - 1) % NU, part[(u + 1) % 2], pf, 0, 6);
+      __builtin_amdgcn_sched_barrier(0);
+      part[u % 2] = mul32<EXACT>(x.b[j][1], x.a[i][1], part[u % 2]);
+      __builtin_amdgcn_sched_barrier(0);
+      join_unit((u + NU - 1) % NU, part[(u + 1) % 2], pf, 6, 16);
+      pf = x.s[i] * x.sb;
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
@@ -382,7 +393,10 @@ __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8Bl
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   Frags x[2];
-  read(0, 0, x[0]);
+#pragma unroll
+  for (int d = 0; d < ND; ++d) read(0, x[0], d);
+  x[0].sb = bs[0];
+  part[1] = (float16v){};
   uint32_t cur = 0;  // s % NST
   auto step = [&](uint32_t s, auto tag) {
     constexpr int C = decltype(tag)::value;
@@ -390,12 +404,18 @@ __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8Bl
     wait_lgkm0();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
     const uint32_t nxt = cur + 1 == NST ? 0 : cur + 1;
-    read(nxt, min(s + 1, KB - 1), x[C ^ 1]);
     const uint32_t kb = min(s + NST, KB - 1);
+    x[C ^ 1].sb = bs[min(s + 1, KB - 1)];
+    multiply(x[C], [&](int u) {
 #pragma unroll
-    for (int q = 0; q < TN; ++q) issue(cur, kb, q);
-    multiply(x[C]);
+      for (int d = 0; d < ND; ++d)
+        if (d * NU / ND == u) read(nxt * STAGE, x[C ^ 1], d);
+#pragma unroll
+      for (int q = 0; q < TN; ++q)
+        if (q * NU / TN == u) issue(cur, kb, q);
+    });
     cur = nxt;
   };
   uint32_t s = 0;
@@ -410,12 +430,13 @@ __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8Bl
     wait_lgkm0();
     if (s + 1 < KB) {
       cut(x[1], K - whole * 128);
-      multiply(x[1]);
+      multiply(x[1], [](int) {});
     }
   } else if (s < KB) {
     cut(x[0], K - whole * 128);
-    multiply(x[0]);
+    multiply(x[0], [](int) {});
   }
+  join_unit(NU - 1, part[1], pf, 0, 16);
   // every transfer has landed and every wave is past its last read: all of LDS
   // is free for the epilogue
   wait_vm<0>();
