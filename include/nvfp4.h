@@ -269,9 +269,11 @@ nvfp4_status nvfp4_fp8_block_quantize(const void *x, nvfp4_dtype x_type,
  *                   * sum_{k = 128b .. 128b+127, k < K} e4m3(A[m][k]) e4m3(B[n][k])
  * A [M x K] activations with scales [M][ceil(K/128)], B [N x K] weights (one
  * row per output feature) with scales [ceil(N/128)][ceil(K/128)], dense
- * row-major E4M3FN bytes, 16-byte aligned; scales finite.  Products inside a
- * block are exact, accumulation is float32 over a block and over the blocks;
- * the result is rounded to c_type.  M, N >= 0; K > 0, K % 16 == 0; c is
+ * row-major E4M3FN bytes, 16-byte aligned; scales finite.  The blocks are
+ * joined in float32 and the result is rounded to c_type.  c_type NVFP4_F32:
+ * products exact, float32 sums.  NVFP4_BF16: products through the FP8 matrix
+ * unit, which cuts each of eight neighbouring products below 2^-13 of the
+ * largest (1.4e-5 of a random result, against the result's own 2^-9).  M, N >= 0; K > 0, K % 16 == 0; c is
  * [M][ldc] of c_type, ldc >= N, aligned to its element.
  * ---------------------------------------------------------------------- */
 nvfp4_status nvfp4_fp8_block_gemm(const uint8_t *a_q, const float *a_s,

@@ -10,13 +10,13 @@
 // the product of its two scales.
 //
 // Which matrix instruction: the FP8 MFMAs of gfx950 (the block-scaled and the
-// older unscaled ones alike) add neighbouring products with about 14 bits below
-// the largest of them (448 * 448 + 14.06 comes out as 448 * 448 + 8; products
-// further apart in K add exactly), which leaves 1.4e-5 of a result of 128 random
-// products.  That vanishes in a bf16 result (2^-9), which uses them; a float32
-// result takes the operands exactly to f16 (E4M3 has 4 significant bits and
-// exponents inside f16's) and the f16 MFMA, whose sums are good to float32, at
-// half the matrix rate.
+// older unscaled ones alike) add the products of eight consecutive K at a common
+// scale, each cut below 2^-13 of 2^(sum of the exponents) of the largest (448 *
+// 448 + 14.06 comes out as 448 * 448 + 8; products further apart in K add
+// exactly), which leaves 1.4e-5 of a result of 128 random products.  That
+// vanishes in a bf16 result (2^-9), which uses them; a float32 result takes the
+// operands exactly to f16 (E4M3 has 4 significant bits and exponents inside
+// f16's) and the f16 MFMA, whose sums are good to float32, at half the matrix rate.
 #include "nvfp4_common.hpp"
 #include "nvfp4_format.hpp"
 #include "nvfp4_kernels.hpp"
@@ -54,18 +54,29 @@ __device__ __forceinline__ half8v halves(const Fp8Frag &f, int j) {
   return (half8v){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// acc += a x b over 64 of K, 32 x 32 (lane half h holds bytes [32h, 32h + 32)
-// of its row of either operand: any K order that both share)
+// A 32 x 64 operand of the 32 x 32 products (lane half h holds bytes [32h, 32h + 32)
+// of its row of either operand: any K order that both share): the bytes
+// themselves, or, for float32 results, their f16 values, converted once.
 template <bool EXACT>
-__device__ __forceinline__ float16v mul32(const Fp8Frag &a, const Fp8Frag &b, float16v acc) {
-  if constexpr (EXACT) {
+struct Operand {
+  i32x8 v;
+  __device__ __forceinline__ explicit Operand(const Fp8Frag &f) : v(joined(f)) {}
+};
+template <>
+struct Operand<true> {
+  half8v v[4];
+  __device__ __forceinline__ explicit Operand(const Fp8Frag &f) : v{halves(f, 0), halves(f, 1), halves(f, 2), halves(f, 3)} {}
+};
+
+// acc += a x b
+__device__ __forceinline__ float16v mul32(const Operand<true> &a, const Operand<true> &b, float16v acc) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(halves(a, j), halves(b, j), acc, 0, 0, 0);
-    return acc;
-  } else {
-    // both operands E4M3 (formats 0), unit block scales (E8M0 127)
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(joined(a), joined(b), acc, 0, 0, 0, 127, 0, 127);
-  }
+  for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a.v[j], b.v[j], acc, 0, 0, 0);
+  return acc;
+}
+__device__ __forceinline__ float16v mul32(const Operand<false> &a, const Operand<false> &b, float16v acc) {
+  // both operands E4M3 (formats 0), unit block scales (E8M0 127)
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a.v, b.v, acc, 0, 0, 0, 127, 0, 127);
 }
 
 // acc += a x b over 128 of K, 16 x 16 (lane quarter q holds bytes [32q, 32q + 32))
@@ -99,112 +110,52 @@ __device__ __forceinline__ Fp8Frag load_frag(const uint8_t *row, uint64_t k, uin
   return f;
 }
 
-// Plain kernel (any K % 16 == 0, 64-bit offsets): a 64 x 64 tile per workgroup,
-// one 32 x 32 MFMA tile per wave, operands loaded from global memory into
-// registers 16 bytes at a time (zero past K).  The weight fragment goes first,
-// so a lane's accumulators are one row of C and its scale one factor.
-template <typename OutT>
-__global__ __launch_bounds__(256) void block_gemm_plain_kernel(Fp8BlockGemmParams p) {
-  const uint32_t tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
-  const uint32_t l32 = lane % 32, lh = lane / 32;
-  const uint32_t tiles_n = (p.N + 63) / 64;
-  const uint32_t row0 = (blockIdx.x / tiles_n) * 64 + (wave / 2) * 32;
-  const uint32_t col0 = (blockIdx.x % tiles_n) * 64 + (wave % 2) * 32;
-  const uint64_t K = p.K;
-  const uint32_t KB = (p.K + 127) / 128;
-  const uint32_t m = min(row0 + l32, p.M - 1), n = min(col0 + l32, p.N - 1);
-  const uint8_t *ar = p.a_q + (uint64_t)m * K, *br = p.b_q + (uint64_t)n * K;
-  const float *as = p.a_s + (uint64_t)m * KB;
-  const float *bs = p.b_s + (uint64_t)(min(col0, p.N - 1) / 128) * KB;  // 32 columns lie in one scale row
-  float16v acc = {};
-  for (uint32_t kb = 0; kb < KB; ++kb) {
-    float16v part = {};
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const uint64_t k = (uint64_t)kb * 128 + 64 * t + 32 * lh;
-      part = mul32<kExact<OutT>>(load_frag(br, k, K), load_frag(ar, k, K), part);
-    }
-    const float f = as[kb] * bs[kb];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = __builtin_fmaf(part[r], f, acc[r]);
-  }
-  // accumulator 4q + e of lane (l32, lh): row l32, column 8q + 4 lh + e
-  OutT *Cp = static_cast<OutT *>(p.c);
-  const uint32_t row = row0 + l32;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const uint32_t col = col0 + 8 * (r / 4) + 4 * lh + (r % 4);
-    if (row < p.M && col < p.N) Cp[(int64_t)row * p.ldc + col] = to_out<OutT>(acc[r]);
-  }
-}
-
-// Few rows (M <= 16 MT): bound by one read of B.  A workgroup owns 16 NR columns
-// of C and its NW waves take the 128-column blocks of K in turn, U blocks' loads
-// in flight together; a weight fragment is used for all MT row tiles.  The waves'
-// sums are joined through LDS in wave order.
-template <int MT, int NR, int NW, int U, typename OutT>
-__global__ __launch_bounds__(NW * 64) void block_gemm_skinny_kernel(Fp8BlockGemmParams p) {
-  __shared__ __attribute__((aligned(16))) float red[NW][MT * 16][NR * 16 + 4];
+// A row or a few (and, with 64-bit offsets, any shape): bound by one read of B.  A
+// workgroup owns 16 columns of 16 rows of C and its NW waves take the 128-column
+// blocks of K in turn, U blocks' loads in flight together, straight into registers
+// (M = 1 reads the same lines of A in every lane group).  The waves' sums are
+// joined through LDS in wave order.
+template <int NW, int U, typename OutT>
+__global__ __launch_bounds__(NW * 64) void block_gemm_rows_kernel(Fp8BlockGemmParams p) {
+  __shared__ __attribute__((aligned(16))) float red[NW][16][20];
   const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64;
   const uint32_t l16 = lane % 16, lq = lane / 16;
-  const uint32_t n0 = blockIdx.x * (16 * NR);
+  const uint32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
   const uint64_t K = p.K;
   const uint32_t KB = (p.K + 127) / 128;
-  const uint8_t *br[NR], *ar[MT];
-  const float *as[MT];
-#pragma unroll
-  for (int i = 0; i < NR; ++i) br[i] = p.b_q + (uint64_t)min(n0 + 16 * i + l16, p.N - 1) * K;
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const uint64_t m = min(16 * j + l16, p.M - 1);
-    ar[j] = p.a_q + m * K;
-    as[j] = p.a_s + m * KB;
-  }
-  const float *bs = p.b_s + (uint64_t)(n0 / 128) * KB;  // 16 NR columns lie in one scale row
-  float4v acc[NR][MT];
-#pragma unroll
-  for (int i = 0; i < NR; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = (float4v){0, 0, 0, 0};
+  const uint64_t m = min(m0 + l16, p.M - 1);
+  const uint8_t *br = p.b_q + (uint64_t)min(n0 + l16, p.N - 1) * K, *ar = p.a_q + m * K;
+  const float *as = p.a_s + m * KB;
+  const float *bs = p.b_s + (uint64_t)(n0 / 128) * KB;  // 16 columns lie in one scale row
+  float4v acc = {0, 0, 0, 0};
   for (uint32_t kb0 = wave; kb0 < KB; kb0 += NW * U) {
-    Fp8Frag fb[U][NR], fa[U][MT];
-    float f[U][MT];
+    Fp8Frag fb[U], fa[U];
+    float f[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t kb = kb0 + NW * u;
       const uint64_t k = (uint64_t)kb * 128 + 32 * lq;
-#pragma unroll
-      for (int i = 0; i < NR; ++i) fb[u][i] = load_frag(br[i], k, K);
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        fa[u][j] = load_frag(ar[j], k, K);
-        f[u][j] = kb < KB ? as[j][kb] * bs[kb] : 0.0f;
-      }
+      fb[u] = load_frag(br, k, K);
+      fa[u] = load_frag(ar, k, K);
+      f[u] = kb < KB ? as[kb] * bs[kb] : 0.0f;
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      const float4v part = mul16<kExact<OutT>>(fb[u], fa[u], (float4v){0, 0, 0, 0});
 #pragma unroll
-      for (int i = 0; i < NR; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          const float4v part = mul16<kExact<OutT>>(fb[u][i], fa[u][j], (float4v){0, 0, 0, 0});
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(part[r], f[u][j], acc[i][j][r]);
-        }
+      for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(part[r], f[u], acc[r]);
+    }
   }
-  // accumulator r of lane (l16, lq): row 16 j + l16, column 16 i + 4 lq + r
-#pragma unroll
-  for (int i = 0; i < NR; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j) *reinterpret_cast<float4v *>(&red[wave][16 * j + l16][16 * i + 4 * lq]) = acc[i][j];
+  // accumulator r of lane (l16, lq): row l16, column 4 lq + r
+  *reinterpret_cast<float4v *>(&red[wave][l16][4 * lq]) = acc;
   __syncthreads();
   OutT *Cp = static_cast<OutT *>(p.c);
-  for (uint32_t c = tid; c < p.M * (16 * NR); c += NW * 64) {
-    const uint32_t m = c / (16 * NR), n = c % (16 * NR);
+  if (tid < 256) {
+    const uint32_t r = tid / 16, n = tid % 16;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) v += red[w][m][n];
-    if (n0 + n < p.N) Cp[(int64_t)m * p.ldc + n0 + n] = to_out<OutT>(v);
+    for (int w = 0; w < NW; ++w) v += red[w][r][n];
+    if (m0 + r < p.M && n0 + n < p.N) Cp[(int64_t)(m0 + r) * p.ldc + n0 + n] = to_out<OutT>(v);
   }
 }
 
@@ -217,6 +168,166 @@ typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 // the fragment reads are 16 consecutive rows at one piece: r % 2 gives the half
 // of a 256-byte window and swz128 a different piece of it for every two rows.
 __device__ __forceinline__ uint32_t swz128(uint32_t r) { return (r >> 1) & 7u; }
+
+// Few rows or few tiles: a (32 FM) x (32 FN) tile of C per workgroup, whose NW
+// waves take the 128-column blocks of K in turn, each alone: it fetches its blocks
+// of A and B straight into NST stages of LDS of its own (1 KB a transfer, whole
+// 128-byte lines), reads the fragments back and multiplies, without a barrier
+// before the waves' sums are joined through LDS, in wave order, at the end.  The
+// work is bound by how fast a compute unit takes in its (32 FM + 32 FN) K bytes,
+// which the depth of the stages (not registers) keeps in flight.  The resources
+// end at the matrix's last row: rows past it cost nothing.
+template <int FM, int FN, int NW, int NST, typename OutT>
+__global__ __launch_bounds__(NW * 64, 1) void block_gemm_strip_kernel(Fp8BlockGemmParams p) {
+  using Op = Operand<kExact<OutT>>;
+  constexpr int BM = 32 * FM, BN = 32 * FN;
+  static_assert(128 % BN == 0, "a tile's columns lie in one scale row");
+  constexpr int TA = BM / 8, TB = BN / 8, TS = (BM + 63) / 64, TN = TA + TB + TS;
+  constexpr int OFF_B = BM * 128, OFF_S = OFF_B + BN * 128, STAGE = OFF_S + TS * 256;
+  constexpr int RED = BN + 4;  // floats per row of a wave's sums
+  constexpr int LDS = NW * NST * STAGE > NW * BM * RED * 4 ? NW * NST * STAGE : NW * BM * RED * 4;
+  static_assert(LDS <= 160 * 1024 && (NST - 1) * TN < 64, "LDS, wait count");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS];
+
+  const uint32_t tid = threadIdx.x;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64;
+  const uint32_t K = p.K, KB = (K + 127) / 128;
+  const uint32_t tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
+  uint32_t tm, tn;
+  dense_tile(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
+  const uint32_t row0 = tm * BM, col0 = tn * BN;
+
+  typedef __amdgpu_buffer_rsrc_t Rsrc;
+  auto rsrc = [](const void *base, uint32_t bytes) -> Rsrc {
+    return __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, (int)bytes, 0x00020000);
+  };
+  const uint32_t rows_a = min(p.M - row0, (uint32_t)BM), rows_b = min(p.N - col0, (uint32_t)BN);
+  const uint8_t *const ta = p.a_q + (size_t)row0 * K, *const tb = p.b_q + (size_t)col0 * K;
+  const float *const ts = p.a_s + (size_t)row0 * KB;
+  // transfer j of an operand: tile rows 8 j + lane / 8, physical piece lane % 8;
+  // the swizzle repeats every 16 rows: two phases
+  uint32_t piece[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) piece[e] = ((lane % 8) ^ swz128(8 * e + lane / 8)) * 16;
+  const uint32_t first = (lane / 8) * K;
+  uint8_t *ring = smem + wave * NST * STAGE;
+  auto issue = [&](uint32_t buf, uint32_t kb) {
+    uint8_t *st = ring + buf * STAGE;
+    const int so = (int)(kb * 128);
+    const uint32_t on = kb < KB ? 1u : 0u;  // past the last block: empty resources, nothing is fetched
+    const Rsrc rA = rsrc(ta, on * rows_a * K), rB = rsrc(tb, on * rows_b * K), rS = rsrc(ts, on * rows_a * KB * 4);
+    uint32_t v[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) v[e] = first + (kb * 128 + piece[e] < K ? piece[e] : 0u);
+#pragma unroll
+    for (int j = 0; j < TB; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(st + OFF_B + j * 1024), 16, (int)(v[j % 2] + j * 8 * K),
+                                               so, 0, 0);
+#pragma unroll
+    for (int j = 0; j < TA; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(st + j * 1024), 16, (int)(v[j % 2] + j * 8 * K), so, 0,
+                                               0);
+#pragma unroll
+    for (int j = 0; j < TS; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rS, (lds_void *)(st + OFF_S + j * 256), 4, (int)((j * 64 + lane) * KB * 4),
+                                               (int)(kb * 4), 0, 0);
+  };
+
+  typedef const float __attribute__((address_space(4))) cfloat;
+  cfloat *bs = (cfloat *)(uintptr_t)(p.b_s + (size_t)(col0 / 128) * KB);
+  const uint32_t l32 = lane % 32, lh = lane / 32;
+  uint32_t off[2][2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) off[t][h] = l32 * 128 + ((4 * t + 2 * lh + h) ^ swz128(l32)) * 16;
+  auto frag = [&](const uint8_t *at, int t, uint32_t left) {
+    Fp8Frag f;
+    f.lo = *reinterpret_cast<const u32x4 *>(at + off[t][0]);
+    f.hi = *reinterpret_cast<const u32x4 *>(at + off[t][1]);
+    if (left < 128) {  // uniform: the last block of a K that is no multiple of 128
+      const uint32_t c = (4 * t + 2 * lh) * 16;
+      if (c >= left) f.lo = (u32x4){0, 0, 0, 0};
+      if (c + 16 >= left) f.hi = (u32x4){0, 0, 0, 0};
+    }
+    return f;
+  };
+
+  float16v acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = (float16v){};
+  // the wave's blocks: wave, wave + NW, ... (past the last one transfers are still
+  // counted, so that one wait count serves every turn)
+#pragma unroll
+  for (int st = 0; st < NST; ++st) issue(st, wave + st * NW);
+  uint32_t buf = 0;
+  for (uint32_t kb = wave; kb < KB; kb += NW) {
+    const float sb = bs[kb];
+    wait_vm<(NST - 1) * TN>();
+    asm volatile("" ::: "memory");
+    const uint8_t *st = ring + buf * STAGE;
+    const uint32_t left = K - kb * 128;
+    Fp8Frag a[FM][2], b[FN][2];
+    float f[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) f[i] = *reinterpret_cast<const float *>(st + OFF_S + (i * 32 + l32) * 4);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) a[i][t] = frag(st + i * 4096, t, left);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) b[j][t] = frag(st + OFF_B + j * 4096, t, left);
+    }
+    wait_lgkm0();  // the stage has been read: it takes the block NST turns ahead
+    asm volatile("" ::: "memory");
+    issue(buf, kb + NST * NW);
+    buf = buf + 1 == NST ? 0 : buf + 1;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) f[i] *= sb;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const Op b0(b[j][0]), b1(b[j][1]);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        float16v part = mul32(b0, Op(a[i][0]), (float16v){});
+        part = mul32(b1, Op(a[i][1]), part);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(part[r], f[i], acc[i][j][r]);
+      }
+    }
+  }
+  wait_vm<0>();
+  __syncthreads();  // every transfer has landed: the stages become the waves' sums
+  float *red = reinterpret_cast<float *>(smem);
+  // accumulator 4q + e of lane (l32, lh): row l32, column 8q + 4 lh + e
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<u32x4 *>(red + (wave * BM + i * 32 + l32) * RED + j * 32 + 8 * q + 4 * lh) =
+            (u32x4){f2u(acc[i][j][4 * q]), f2u(acc[i][j][4 * q + 1]), f2u(acc[i][j][4 * q + 2]),
+                    f2u(acc[i][j][4 * q + 3])};
+  __syncthreads();
+  OutT *Cp = static_cast<OutT *>(p.c);
+  for (uint32_t c = tid; c < rows_a * (BN / 4); c += NW * 64) {
+    const uint32_t m = c / (BN / 4), n = c % (BN / 4) * 4;
+    float4v v = *reinterpret_cast<const float4v *>(red + m * RED + n);
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+      const float4v o = *reinterpret_cast<const float4v *>(red + (w * BM + m) * RED + n);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += o[e];
+    }
+    OutT *gp = Cp + (int64_t)(row0 + m) * p.ldc + col0 + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < rows_b) gp[e] = to_out<OutT>(v[e]);
+  }
+}
 
 // Many rows: a BM x BN tile per workgroup, NWM x NWN waves of 64 x WN each.
 //  * One step is one 128-column block: its tiles of A and B (128 bytes a row) and
@@ -244,7 +355,7 @@ __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8Bl
   constexpr int TA = BM / 8 / NW, TB = BN / 8 / NW;  // transfers of 8 rows per wave and step
   constexpr int TN = TA + TB + 1;
   constexpr int OFF_B = BM * 128, OFF_S = OFF_B + BN * 128, STAGE = OFF_S + NW * 256;
-  constexpr bool EXACT = kExact<OutT>;
+  using Op = Operand<kExact<OutT>>;
   static_assert(NST * STAGE <= 160 * 1024, "LDS");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NST * STAGE];
 
@@ -262,9 +373,8 @@ __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8Bl
     return __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, (int)bytes, 0x00020000);
   };
   const uint32_t rows_a = min(p.M - row0, (uint32_t)BM), rows_b = min(p.N - col0, (uint32_t)BN);
-  const Rsrc rA = rsrc(p.a_q + (size_t)row0 * K, rows_a * K);
-  const Rsrc rB = rsrc(p.b_q + (size_t)col0 * K, rows_b * K);
-  const Rsrc rS = rsrc(p.a_s + (size_t)row0 * KB, rows_a * KB * 4);
+  const uint8_t *const ta = p.a_q + (size_t)row0 * K, *const tb = p.b_q + (size_t)col0 * K;
+  const float *const ts = p.a_s + (size_t)row0 * KB;
   // transfer j of an operand: tile rows (j NW + wave) * 8 + lane / 8, physical
   // piece lane % 8 (the swizzle repeats every 16 rows: the same for every j when
   // 8 NW is a multiple of 16)
@@ -273,11 +383,14 @@ __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8Bl
   const uint32_t piece = ((lane % 8) ^ swz128(trow)) * 16;
   const uint32_t first = trow * K;
   const uint32_t srow = (wm * 64 + lane) * KB * 4;
+  const uint32_t size_a = rows_a * K, size_b = rows_b * K, size_s = rows_a * KB * 4;
   // the transfers of block kb into stage buf; q-th of TN
   auto issue = [&](uint32_t buf, uint32_t kb, int q) {
     uint8_t *st = smem + buf * STAGE;
     const uint32_t v = first + (kb * 128 + piece < K ? piece : 0u);
     const int so = (int)(kb * 128);
+    const bool on = kb < KB;  // past the last block: empty resources, nothing is fetched
+    const Rsrc rA = rsrc(ta, on ? size_a : 0u), rB = rsrc(tb, on ? size_b : 0u), rS = rsrc(ts, on ? size_s : 0u);
     if (q < TA)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(st + (q * NW + wave) * 1024), 16,
                                                (int)(v + q * (NW * 8) * K), so, 0, 0);
@@ -367,12 +480,12 @@ __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8Bl
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       const int i = u % FM, j = u / FM;
-      part[u % 2] = mul32<EXACT>(x.b[j][0], x.a[i][0], (float16v){});
+      part[u % 2] = mul32(Op(x.b[j][0]), Op(x.a[i][0]), (float16v){});
       __builtin_amdgcn_sched_barrier(0);
       under(u);
       join_unit((u + NU - 1) % NU, part[(u + 1) % 2], pf, 0, 6);
       __builtin_amdgcn_sched_barrier(0);
-      part[u % 2] = mul32<EXACT>(x.b[j][1], x.a[i][1], part[u % 2]);
+      part[u % 2] = mul32(Op(x.b[j][1]), Op(x.a[i][1]), part[u % 2]);
       __builtin_amdgcn_sched_barrier(0);
       join_unit((u + NU - 1) % NU, part[(u + 1) % 2], pf, 6, 16);
       pf = x.s[i] * x.sb;
@@ -383,12 +496,12 @@ __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8Bl
   // Step s: its fragments are in registers; stage s + 1 has landed (own
   // transfers waited for, then the barrier for everyone's), and buffer s % NST is
   // free (its reads were waited for before the barrier): it takes block s + NST.
-  // Past the end the last block is fetched again, into a stage nobody reads, so
-  // that one wait count serves every step.
+  // Past the end transfers fetch nothing but are still counted, so that one wait
+  // count serves every step.
 #pragma unroll
   for (int st = 0; st < NST; ++st)
 #pragma unroll
-    for (int q = 0; q < TN; ++q) issue(st, min((uint32_t)st, KB - 1), q);
+    for (int q = 0; q < TN; ++q) issue(st, st, q);
   wait_vm<(NST - 1) * TN>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -406,7 +519,7 @@ __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8Bl
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     const uint32_t nxt = cur + 1 == NST ? 0 : cur + 1;
-    const uint32_t kb = min(s + NST, KB - 1);
+    const uint32_t kb = s + NST;
     x[C ^ 1].sb = bs[min(s + 1, KB - 1)];
     multiply(x[C], [&](int u) {
 #pragma unroll
@@ -506,9 +619,10 @@ __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8Bl
   }
 }
 
-template <int MT, int NR, int NW, int U, typename OutT>
-hipError_t launch_skinny(const Fp8BlockGemmParams &p, hipStream_t stream) {
-  block_gemm_skinny_kernel<MT, NR, NW, U, OutT><<<(p.N + 16 * NR - 1) / (16 * NR), NW * 64, 0, stream>>>(p);
+template <int FM, int FN, int NW, int NST, typename OutT>
+hipError_t launch_strip(const Fp8BlockGemmParams &p, hipStream_t stream) {
+  const uint32_t grid = ((p.M + 32 * FM - 1) / (32 * FM)) * ((p.N + 32 * FN - 1) / (32 * FN));
+  block_gemm_strip_kernel<FM, FN, NW, NST, OutT><<<grid, NW * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -522,18 +636,49 @@ hipError_t launch_tile(const Fp8BlockGemmParams &p, hipStream_t stream) {
 }
 
 template <typename OutT>
-hipError_t launch_typed(const Fp8BlockGemmParams &p, hipStream_t stream) {
-  if (p.M <= 16) return launch_skinny<1, 1, 8, 4, OutT>(p, stream);
-  if (p.M <= 32) return launch_skinny<2, 2, 8, 2, OutT>(p, stream);
-  if (p.M <= 64) return launch_skinny<4, 2, 8, 1, OutT>(p, stream);
-  // the tile kernel's resources hold 256 rows: 32-bit offsets
-  if ((uint64_t)p.K * 256 < (1ull << 32)) {
-    if (p.M <= 128) return launch_tile<128, 128, 2, 2, 4, OutT>(p, stream);
-    return launch_tile<128, 256, 2, 2, 3, OutT>(p, stream);
-  }
-  const uint64_t grid = (uint64_t)((p.M + 63) / 64) * ((p.N + 63) / 64);
-  block_gemm_plain_kernel<OutT><<<(uint32_t)grid, 256, 0, stream>>>(p);
+hipError_t launch_rows(const Fp8BlockGemmParams &p, hipStream_t stream) {
+  const uint64_t grid_m = ((uint64_t)p.M + 15) / 16;
+  if (grid_m > 65535) return hipErrorInvalidValue;
+  block_gemm_rows_kernel<16, 2, OutT><<<dim3((p.N + 15) / 16, (uint32_t)grid_m), 1024, 0, stream>>>(p);
   return hipGetLastError();
+}
+
+// Which kernel, and which tile: the largest one that still gives most compute
+// units a workgroup (tiles >= 0.6 of them), since a unit takes its operands in at
+// a bounded rate (about 45 GB/s each) and a larger tile takes in less per output.
+// Measured with K = 5120 (us, this choice first, then the neighbours it beat):
+//   M x N         tile            us     others
+//   1024 x 5120   128 x 256       44.5   128 x 128 56.8, 64 x 64 53
+//   512 x 5120    128 x 128       26.7   128 x 256 48, 64 x 64 32.6
+//   256 x 5120    64 x 128        23.0   128 x 128 30, 64 x 64 22.7
+//   128 x 25600   128 x 128       47.2   128 x 256 58, 64 x 64 57
+//   128 x 5120    64 x 64         14.5   128 x 128 28, 32 x 64 16.4
+//   64 x 25600    64 x 128        37.2   64 x 64 42
+//   64 x 5120     32 x 64         10.8   64 x 64 15.2, 32 x 32 13.3
+//   32 x 25600    32 x 128        30.8   32 x 64 33.5
+//   32 x 5120     32 x 32         9.5    32 x 64 11.0
+//   1 x 2048 (K 2048)  rows       4.1    32 x 32 5.1
+// A float32 result (f16 products, converted operands) skips 64 x 128: 1000 x 1552
+// x 2064 takes 15.5 with 64 x 64 and 22.7 with 64 x 128.
+template <typename OutT>
+hipError_t launch_typed(const Fp8BlockGemmParams &p, hipStream_t stream) {
+  // the tiles' resources hold up to 256 rows: 32-bit offsets
+  if (p.M <= 4 || (uint64_t)p.K * 256 >= (1ull << 32)) return launch_rows<OutT>(p, stream);
+  const uint64_t enough = device_cu_count() * 3 / 5;
+  auto fills = [&](uint64_t bm, uint64_t bn) { return ((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn) >= enough; };
+  if (p.M > 64) {
+    if (fills(128, 256)) return launch_tile<128, 256, 2, 2, 3, OutT>(p, stream);
+    if (fills(128, 128)) return launch_tile<128, 128, 2, 2, 3, OutT>(p, stream);
+  }
+  if (p.M > 32) {
+    if constexpr (!kExact<OutT>)
+      if (fills(64, 128)) return launch_tile<64, 128, 1, 2, 3, OutT>(p, stream);
+    if (fills(64, 64)) return launch_strip<2, 2, 4, 1, OutT>(p, stream);
+    if (fills(32, 64)) return launch_strip<1, 2, 8, 1, OutT>(p, stream);
+  } else if (fills(32, 128)) {
+    return launch_strip<1, 4, 2, 2, OutT>(p, stream);
+  }
+  return launch_strip<1, 1, 8, 1, OutT>(p, stream);
 }
 
 }  // namespace

@@ -1,8 +1,9 @@
 """GPU parity of the block-scaled FP8 quantize and GEMM against their oracle.
 
 Quantized bytes and scales are bit-exact.  GEMM outputs lie within the oracle's bound on a
-float32 evaluation, element by element; a bf16 output half a bf16 step (2^-8 relative at
-most) further.
+float32 evaluation, element by element; a bf16 output, whose products go through the FP8
+matrix unit, within the bound that counts that unit's cuts, half a bf16 step (2^-8 relative
+at most) further, and as a whole within half a bf16 step in norm (the cuts are 2^-16 there).
 """
 
 import numpy as np
@@ -109,14 +110,16 @@ def _check(B, M, N, K, dtype, out=None, a=None, b=None, seed=0):
     a, b = a or a0, b or b0
     y = B.nvfp4_fp8_block_gemm(a, b, out_dtype=dtype, out=out)
     args = [t.cpu().numpy() for t in (*a, *b)]
-    ref, tol = P.gemm(*args), P.gemm_bound(*args)
-    if dtype == torch.bfloat16:
+    bf16 = dtype == torch.bfloat16
+    ref, tol = P.gemm(*args), P.gemm_bound(*args, fp8_unit=bf16)
+    if bf16:
         tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
     err = np.abs(y.double().cpu().numpy() - ref)
     worst = np.max(err / np.maximum(tol, 1e-300))
     rel = np.linalg.norm(err) / max(np.linalg.norm(ref), 1e-300)
     print(f"[fp8 block gemm] {M}x{N}x{K} {dtype}: {worst:.3f} of the bound, rel {rel:.2e}", flush=True)
     assert worst <= 1.0, (M, N, K, worst)
+    assert not bf16 or rel <= 2.0 ** -8, (M, N, K, rel)
     return y
 
 
@@ -129,6 +132,31 @@ SHAPES = [(1, 1, 16), (1, 512, 512), (2, 17, 144), (7, 130, 272), (16, 256, 5120
 @pytest.mark.parametrize("M,N,K", SHAPES)
 def test_gemm(B, M, N, K, dtype):
     _check(B, M, N, K, dtype)
+
+
+# Every tile that the launch chooses from (256 compute units): few tiles to many, each with rows and
+# columns that end inside a tile and a K that ends inside a block
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(4, 100, 400), (5, 100, 400), (20, 19900, 272), (60, 5100, 400), (61, 19700, 272),
+                                   (130, 4990, 400), (257, 6600, 272), (1150, 4500, 400), (64, 10000, 144)])
+def test_gemm_every_tile(B, M, N, K, dtype):
+    _check(B, M, N, K, dtype)
+
+
+def test_gemm_long_k(B):
+    """K past the tile kernels' 32-bit offsets (256 rows of 2^24 bytes)."""
+    M, N, K = 6, 3, 2 ** 24 + 144
+    a, b = _operands(M, N, K, 12)
+    y = B.nvfp4_fp8_block_gemm(a, b, out_dtype=torch.float32)
+
+    def values(t, rows):
+        s = t[1].double().repeat_interleave(rows, 0)[:t[0].shape[0]]
+        return t[0].view(torch.float8_e4m3fn).double() * s.repeat_interleave(128, 1)[:, :K]
+
+    av, bv = values(a, 1), values(b, 128)
+    ref = torch.stack([(av * row).sum(1) for row in bv], 1)
+    tol = (128 + K // 128 + 4) * 2.0 ** -23 * torch.stack([(av * row).abs().sum(1) for row in bv], 1)
+    assert torch.all((y.double() - ref).abs() <= tol)
 
 
 @pytest.mark.parametrize("M", [1, 5, 40, 200])

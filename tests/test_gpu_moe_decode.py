@@ -172,7 +172,7 @@ def test_decode_step(B):
     for a, w, got in ((x, wp, hid), (hid, wr, logits)):
         aq = P.quantize(a.float().cpu().numpy())
         wq = [t.cpu().numpy() for t in w]
-        ref, tol = P.gemm(*aq, *wq), P.gemm_bound(*aq, *wq)
+        ref, tol = P.gemm(*aq, *wq), P.gemm_bound(*aq, *wq, fp8_unit=got.dtype == torch.bfloat16)
         if got.dtype == torch.bfloat16:
             tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
         assert np.all(np.abs(got.double().cpu().numpy() - ref) <= tol)
