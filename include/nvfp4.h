@@ -386,9 +386,11 @@ nvfp4_status nvfp4_moe_combine(const void *y, nvfp4_dtype y_type,
  *   h_j = SiLU(Wg[e_j] x) * (Wu[e_j] x);  out = sum_{j<k} w_j * Wd[e_j] h_j
  * Weights are NVFP4; the activations x and h are NOT quantized (with few tokens
  * the layer is bound by the selected experts' bytes, each read once), so the
- * result is that of the dequantized weights in float32: h is carried to the
- * full 24 bits when out is float32 and to 2^-18 when out is bfloat16.  For many
- * tokens use the routed calls above.
+ * result is that of the dequantized weights with float32 sums: x and h are
+ * carried to 2^-22 of a value when they or out are float32; a bfloat16 x is taken
+ * as it is, and h is carried to 2^-11 when out is bfloat16 (2^-8); nothing below
+ * 2^-39 of the largest value of a token's x or of one slot's h is kept.  For
+ * many tokens use the routed calls above.
  *
  * x       [T][ld_x] of x_type (f32 or bf16), ld_x >= H (elements).
  * logits  float [T][E], dense.

@@ -497,12 +497,11 @@ nvfp4_status nvfp4_moe_decode(const void *x, nvfp4_dtype x_type, int64_t ld_x, c
   p.gu_q = gu_q; p.gu_s = gu_s; p.gu_g = gu_g;
   p.d_q = d_q; p.d_s = d_s; p.d_g = d_g;
   p.out = out; p.ld_out = ld_out;
-  const bool x_vec = aligned16(x) && (ld_x * (int64_t)dtype_size(x_type)) % 16 == 0;
   // 16-byte code loads and 4-byte scale loads: 64 elements of a row at a time
   const bool gu_aligned = H % 64 == 0 && aligned16(gu_q) && ((uintptr_t)gu_s & 3u) == 0;
   const bool d_aligned = I % 64 == 0 && aligned16(d_q) && ((uintptr_t)d_s & 3u) == 0;
-  return from_hip(launch_moe_decode(p, x_type == NVFP4_BF16, x_vec, gu_aligned, d_aligned, out_type == NVFP4_BF16,
-                                    workspace, stream));
+  return from_hip(launch_moe_decode(p, x_type == NVFP4_BF16, gu_aligned, d_aligned, out_type == NVFP4_BF16, workspace,
+                                    stream));
 }
 
 }  // extern "C"

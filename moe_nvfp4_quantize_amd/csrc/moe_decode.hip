@@ -9,12 +9,11 @@
 // and the two quantizations of moe_layer (and what they round away) fall out.
 //
 // Launches, none of which waits for another on the host:
-//   1. prep (more than kFuseT tokens, or x to be split): a wave per token finds its
-//      experts; x is split into planes (below) where the products need it.
-//   2. gate_up: one workgroup per (expert, 16 rows of h); its waves split the hidden
-//      dimension and join through LDS; SiLU gate; h to the workspace.  With up to
-//      kFuseT tokens every workgroup finds the tokens' experts itself.
-//   3. down: one workgroup per (expert, 64 rows of out), its products times the
+//   1. prep: a wave per token finds its experts; a workgroup per token writes x as
+//      f16 (below).
+//   2. gate_up: one workgroup per (expert, 16 RT rows of h); its waves split the
+//      hidden dimension and join through LDS; SiLU gate; h to the workspace as f16.
+//   3. down: one workgroup per (expert, 64 RT rows of out), its products times the
 //      routing weight to the workspace, and
 //   4. combine: the sum over a token's experts, in slot order.
 //      Up to kOwnSlots slots: instead one kernel whose workgroups own 16 rows of out,
@@ -24,13 +23,17 @@
 // (or, with more slots than experts, an expert, and leaves if no slot has it), and
 // finds the tokens of its expert by comparing all slots, a few ballots.
 //
-// Products: bf16 MFMA (16 weight rows x 16 columns x 32 of K) with float32
-// accumulation.  A weight e2m1 * e4m3 has at most 6 significant bits, so it is
-// exact in bf16.  A float32 operand is split into bf16 planes whose sum it is
-// (three planes: exactly; two: to 2^-18), each plane a column of its own: with
-// few tokens an expert's columns are mostly free, so the planes cost no further
-// matrix instruction.  Three planes are used for float32 results, two planes of h
-// where the output is rounded to bf16 (2^-9) anyway.
+// Products: f16 MFMA (16 weight rows x 16 columns x 32 of K) with float32
+// accumulation.  A weight e2m1 * e4m3 is exact in f16 (as in gemm.hip) and decodes
+// in eight packed instructions per eight codes; bf16, which needs the products
+// formed in float32, took sixteen and 30% longer for the layer.  Activations come
+// to f16 under a power of two of their own, which the result is multiplied by in
+// float32: x per token, its largest value in [2^14, 2^15); h per 16 rows of a
+// slot, where gate_up has it in hand, and down brings a slot's blocks to its
+// largest one's power as it reads them.  What a value loses by that is below
+// 2^-39 of its row's largest.  A float32 value is two f16 planes whose sum it is to
+// 2^-22, each a column of its own; h is one plane (2^-11) where the output is
+// rounded to bf16 (2^-8) anyway.
 #include "nvfp4_common.hpp"
 #include "nvfp4_format.hpp"
 #include "nvfp4_kernels.hpp"
@@ -40,13 +43,17 @@ namespace nvfp4 {
 
 namespace {
 
-typedef float float2v __attribute__((ext_vector_type(2)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half8v __attribute__((ext_vector_type(8)));
 
 constexpr int CH = 256;  // K elements per wave step: 64 per lane quarter
 
+#ifndef RTG_MIN
+#define RTG_MIN 4
+#define RTD_MIN 8
+#endif
 // ------------------------------------------------------------------- route
 
 // maximum over the wave, in every lane (scalar): rows of 16 by rotations, then
@@ -130,27 +137,21 @@ __device__ __forceinline__ void topk_any(const float *row, uint32_t E, uint32_t 
   else topk_row<16>(row, E, k, id, w);
 }
 
-// float32 -> P bf16 planes whose sum it is: each plane but the last of two is
-// cut (not rounded), so that what remains is exact
+// float32 -> P f16 planes whose sum it is
 template <int P>
-__device__ __forceinline__ void split(float v, uint16_t out[P]) {
-  if constexpr (P == 1) {
-    out[0] = (uint16_t)float_to_bf16_bits(v);
-  } else if constexpr (P == 2) {
-    out[0] = (uint16_t)float_to_bf16_bits(v);
-    out[1] = (uint16_t)float_to_bf16_bits(v - u2f((uint32_t)out[0] << 16));
-  } else {
-    const float a = u2f(f2u(v) & 0xFFFF0000u), r = v - a;
-    const float b = u2f(f2u(r) & 0xFFFF0000u), c = r - b;
-    out[0] = (uint16_t)(f2u(a) >> 16);
-    out[1] = (uint16_t)(f2u(b) >> 16);
-    out[2] = (uint16_t)(f2u(c) >> 16);
-  }
+__device__ __forceinline__ void split(float v, _Float16 out[P]) {
+  out[0] = (_Float16)v;
+  if constexpr (P == 2) out[1] = (_Float16)(v - (float)out[0]);
 }
 
-// The first p.topk_blocks workgroups: routing, a wave per token.  The others: x into
-// bf16 planes of stride H, 256 elements each: float32 x (P = 3) or bf16 x whose rows
-// are not 16-byte aligned (P = 1).
+// the power p with amax 2^-p in [2^14, 2^15); kNoPower where amax is 0
+constexpr int32_t kNoPower = -128;
+__device__ __forceinline__ int32_t power_of(float amax) {
+  return amax == 0.0f ? kNoPower : max(__builtin_amdgcn_frexp_expf(amax) - 15, kNoPower + 1);
+}
+
+// The first p.topk_blocks workgroups: routing, a wave per token.  The others: a
+// token's x, as P f16 planes of stride H and its power.
 template <int P>
 __global__ __launch_bounds__(256) void decode_prep_kernel(MoeDecodeParams p) {
   if (blockIdx.x < p.topk_blocks) {
@@ -165,31 +166,49 @@ __global__ __launch_bounds__(256) void decode_prep_kernel(MoeDecodeParams p) {
     }
     return;
   }
-  const uint32_t b = blockIdx.x - p.topk_blocks, per = (p.H + 255) / 256;
-  const uint32_t t = b / per, h = (b % per) * 256 + threadIdx.x;
-  if (h >= p.H) return;
-  uint16_t o[P];
-  if constexpr (P == 1) o[0] = ((const uint16_t *)p.x)[(int64_t)t * p.ld_x + h];
-  else split<P>(((const float *)p.x)[(int64_t)t * p.ld_x + h], o);
+  const uint32_t t = blockIdx.x - p.topk_blocks;
+  auto load = [&](uint32_t h) {
+    if constexpr (P == 1) return u2f((uint32_t)((const uint16_t *)p.x)[(int64_t)t * p.ld_x + h] << 16);
+    else return ((const float *)p.x)[(int64_t)t * p.ld_x + h];
+  };
+  constexpr int U = 16;  // elements a thread keeps: rows up to 4096 are read once
+  float v[U];
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < P; ++i) p.xp[((int64_t)i * p.T + t) * p.H + h] = o[i];
+  for (int i = 0; i < U; ++i) {
+    const uint32_t h = i * 256 + threadIdx.x;
+    v[i] = h < p.H ? load(h) : 0.0f;
+    m = fmaxf(m, fabsf(v[i]));
+  }
+  for (uint32_t h = U * 256 + threadIdx.x; h < p.H; h += 256) m = fmaxf(m, fabsf(load(h)));
+  const int32_t e = power_of(block_max(m));
+  if (threadIdx.x == 0) p.xe[t] = e;
+  auto store = [&](uint32_t h, float x) {
+    _Float16 o[P];
+    split<P>(__builtin_ldexpf(x, -e), o);
+#pragma unroll
+    for (int i = 0; i < P; ++i) p.xp[((int64_t)i * p.T + t) * p.H + h] = o[i];
+  };
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const uint32_t h = i * 256 + threadIdx.x;
+    if (h < p.H) store(h, v[i]);
+  }
+  for (uint32_t h = U * 256 + threadIdx.x; h < p.H; h += 256) store(h, load(h));
 }
 
 // ---------------------------------------------------------------- products
 
-// 8 E2M1 codes (one dword) times the block scale s -> 8 exact bf16: converted to
-// float32 in pairs, multiplied (exact: 6 significant bits), and the high halves
-// packed
-__device__ __forceinline__ bf16x8 decode8(uint32_t w, float s) {
-  uint32_t o[4];
-  auto pair = [&](float2v v) {
-    return __builtin_amdgcn_perm(f2u(v[1] * s), f2u(v[0] * s), 0x07060302u);
-  };
-  o[0] = pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0));
-  o[1] = pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1));
-  o[2] = pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2));
-  o[3] = pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3));
-  return __builtin_bit_cast(bf16x8, (u32x4){o[0], o[1], o[2], o[3]});
+// 8 E2M1 codes (one dword) times their block scale -> 8 exact f16.  An E4M3 byte
+// moved up by 7 bits is the f16 encoding of the scale / 256, which the code
+// conversion's power of two makes up for.
+__device__ __forceinline__ half8v decode8(uint32_t w, _Float16 s) {
+  const half2v s2 = {s, s};
+  const half2v p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 0) * s2;
+  const half2v p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 1) * s2;
+  const half2v p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 2) * s2;
+  const half2v p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 3) * s2;
+  return (half8v){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
 // What a lane holds of 16 weight rows for one 256-wide step: 64 codes of its row
@@ -239,30 +258,75 @@ __device__ __forceinline__ Codes load_codes(const uint8_t *q, const uint8_t *s, 
   return c;
 }
 
-// a lane's column: elements [k + 8j, k + 8j + 8) of one bf16 row
-__device__ __forceinline__ bf16x8 load_column(const uint16_t *x, bool in, uint32_t k, uint32_t K, int j) {
-  u32x4 v = {0, 0, 0, 0};
-  if (in && k + 8 * j < K) v = *reinterpret_cast<const u32x4 *>(x + k + 8 * j);
-  return __builtin_bit_cast(bf16x8, v);
+// the j-th of a step's eight 16-row fragments
+__device__ __forceinline__ half8v weights(const Codes &c, int j) {
+  const half2v even = __builtin_bit_cast(half2v, (c.s & 0x00FF00FFu) << 7);         // blocks 0 and 2
+  const half2v odd = __builtin_bit_cast(half2v, ((c.s >> 8) & 0x00FF00FFu) << 7);   // blocks 1 and 3
+  const int b = j / 2;
+  return decode8(j < 4 ? c.lo[j] : c.hi[j - 4], b % 2 ? odd[b / 2] : even[b / 2]);
 }
 
-template <int J>
-__device__ __forceinline__ float scale_at(uint32_t s) { return __builtin_amdgcn_cvt_f32_fp8((int)s, J); }
+// A lane's column in column tile i: its row of f16 values, and, for h, the powers
+// of its blocks of 16 and their largest.
+struct ColumnData {
+  const _Float16 *row;
+  const int8_t *powers;
+  int32_t top;
+  bool in;
+};
 
-// the j-th of a step's eight 16-row fragments
-__device__ __forceinline__ bf16x8 weights(const Codes &c, int j) {
-  const uint32_t w = j < 4 ? c.lo[j] : c.hi[j - 4];
-  const float s = j < 2 ? scale_at<0>(c.s) : j < 4 ? scale_at<1>(c.s) : j < 6 ? scale_at<2>(c.s) : scale_at<3>(c.s);
-  return decode8(w, s);
+// acc[m][i] += 16 rows of matrix m x column tile i, over the steps k0 = first, first +
+// turn, ... of 256 each.  POWERS: each block of the column is brought to its row's
+// largest power.
+template <int NM, int NT, bool ALIGNED, bool POWERS>
+__device__ __forceinline__ void products(const uint8_t *const (&q)[NM], const uint8_t *const (&s)[NM],
+                                         const ColumnData (&x)[NT], uint32_t K, uint32_t first, uint32_t turn,
+                                         float4v (&acc)[NM][NT]) {
+  const uint32_t kq = (threadIdx.x % 64) / 16 * 64;
+  for (uint32_t k0 = first; k0 < K; k0 += turn) {
+    const uint32_t k = k0 + kq;
+    Codes c[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) c[m] = load_codes<ALIGNED>(q[m], s[m], k, K, k0 + CH <= K);
+    half8v f[NT][8];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u32x4 v = {0, 0, 0, 0};
+        if (x[i].in && k + 8 * j < K) v = *reinterpret_cast<const u32x4 *>(x[i].row + k + 8 * j);
+        f[i][j] = __builtin_bit_cast(half8v, v);
+      }
+      if constexpr (POWERS) {
+        // a row of powers is padded to 16 bytes, so the four of 64 elements are one load
+        const uint32_t w = x[i].in && k < K ? *reinterpret_cast<const uint32_t *>(x[i].powers + k / 16) : 0u;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int32_t d = min((int32_t)(int8_t)(w >> (8 * b)) - x[i].top, 0);  // (blocks past K: anything)
+          const _Float16 h = __builtin_amdgcn_ldexph((_Float16)1.0f, d);  // 0 below 2^-24
+#pragma unroll
+          for (int j = 2 * b; j < 2 * b + 2; ++j) f[i][j] *= (half8v){h, h, h, h, h, h, h, h};
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        const half8v w = weights(c[m], j);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, f[i][j], acc[m][i], 0, 0, 0);
+      }
+  }
 }
 
 __device__ __forceinline__ float silu(float z) {
   return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * 1.44269504088896341f));
 }
 
-// P bf16 planes per token share the 16 columns: 16, 8 or 5 tokens at a time
+// P planes per token share the 16 columns
 template <int P>
-constexpr uint32_t kTokens = P == 1 ? 16 : P == 2 ? 8 : 5;
+constexpr uint32_t kTokens = 16 / P;
 
 // The tokens of an expert: ranks [from, from + N) of the slots that have it, in
 // slot order, into list[0 .. N) (the wave's own LDS); returns how many slots have
@@ -272,15 +336,20 @@ __device__ __forceinline__ uint32_t find_tokens(const int32_t *ids, uint32_t S, 
   const uint32_t lane = threadIdx.x % 64;
   uint32_t n = 0;
   *first = S;
-  for (uint32_t s0 = 0; s0 < S; s0 += 64) {
-    const uint32_t s = s0 + lane;
-    const bool mine = s < S && ids[s] == e;
-    const unsigned long long m = __ballot(mine);
-    if (m == 0) continue;
-    if (n == 0) *first = s0 + (uint32_t)__builtin_ctzll(m);
-    const uint32_t rank = n + (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
-    if (mine && rank >= from && rank < from + N) list[rank - from] = s;
-    n += (uint32_t)__popcll(m);
+  for (uint32_t s0 = 0; s0 < S; s0 += 512) {
+    int32_t id[8];  // in flight together
+#pragma unroll
+    for (int i = 0; i < 8; ++i) id[i] = s0 + i * 64 + lane < S ? ids[s0 + i * 64 + lane] : -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const unsigned long long m = __ballot(id[i] == e);
+      if (m == 0) continue;
+      const uint32_t s = s0 + i * 64 + lane;
+      if (n == 0) *first = s0 + i * 64 + (uint32_t)__builtin_ctzll(m);
+      const uint32_t rank = n + (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
+      if (id[i] == e && rank >= from && rank < from + N) list[rank - from] = s;
+      n += (uint32_t)__popcll(m);
+    }
   }
   // written and read by the same wave
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -296,108 +365,104 @@ struct Column {
   bool in;
   __device__ __forceinline__ Column(const uint32_t *list, uint32_t i, uint32_t cnt) {
     const uint32_t l16 = threadIdx.x % 16, c = i * kTokens<P> + l16 % kTokens<P>;
-    in = l16 / kTokens<P> < (uint32_t)P && c < cnt;
+    in = c < cnt;
     slot = in ? list[c] : 0u;
   }
 };
 
-constexpr uint32_t kFuseT = 4;    // tokens up to which gate_up routes by itself
 constexpr uint32_t kOwnSlots = 16;  // slots up to which one kernel does down and combine
 
-// PX planes of x, PH planes of h, NT tiles of 16 columns a pass
-template <int PX, int PH, int NT, bool ALIGNED, bool FUSE>
+// PX planes of x, PH planes of h, NT tiles of 16 columns a pass, RT tiles of 16 rows
+// of h a workgroup
+template <int PX, int PH, int NT, int RT, bool ALIGNED>
 __global__ __launch_bounds__(256) void decode_gate_up_kernel(MoeDecodeParams p) {
-  constexpr uint32_t TP = kTokens<PX>, N = NT * TP, NW = 4;
-  __shared__ __attribute__((aligned(16))) float red[NW][2][NT * 16][20];  // [wave][gate, up][column][row]
+  constexpr uint32_t TP = kTokens<PX>, N = NT * TP, NW = 4, NM = 2 * RT;
+  __shared__ __attribute__((aligned(16))) float red[NW][NM][NT * 16][20];  // [wave][gates, ups][column][row]
   __shared__ uint32_t lists[NW][N];
-  __shared__ int32_t own_ids[FUSE ? kFuseT * 32 : 1];
   const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64;
   const uint32_t l16 = lane % 16, lq = lane / 16;
-  const uint32_t item = blockIdx.x / p.tiles_i, r0 = (blockIdx.x % p.tiles_i) * 16;
-  const int32_t *ids = p.ids;
-  if constexpr (FUSE) {
-    if (wave < p.T) {
-      int32_t id;
-      float w;
-      topk_any(p.logits + (int64_t)wave * p.E, p.E, p.k, &id, &w);
-      if (lane < p.k) {
-        own_ids[wave * p.k + lane] = id;
-        if (blockIdx.x == 0) {  // for the kernels behind this one
-          p.ids[wave * p.k + lane] = id;
-          p.w[wave * p.k + lane] = w;
-        }
-      }
-    }
-    __syncthreads();
-    ids = own_ids;
-  }
-  const int32_t e = __builtin_amdgcn_readfirstlane(p.S <= p.E ? ids[item] : (int32_t)item);
+  const uint32_t item = blockIdx.x / p.tiles_i, r0 = (blockIdx.x % p.tiles_i) * (16 * RT);
+  const int32_t e = __builtin_amdgcn_readfirstlane(p.S <= p.E ? p.ids[item] : (int32_t)item);
   uint32_t *list = lists[wave];
   uint32_t first;
-  const uint32_t total = find_tokens(ids, p.S, e, 0, N, list, &first);
+  const uint32_t total = find_tokens(p.ids, p.S, e, 0, N, list, &first);
   if (total == 0 || (p.S <= p.E && first != item)) return;  // the same in every wave
   const uint32_t K = p.H, I = p.I;
-  const uint64_t row = (uint64_t)e * 2 * I + r0 + l16;  // I % 16 == 0: whole row tiles
-  const uint8_t *gq = p.gu_q + row * (K / 2), *gs = p.gu_s + row * (K / 16);
-  const uint8_t *uq = gq + (uint64_t)I * (K / 2), *us = gs + (uint64_t)I * (K / 16);
+  const uint8_t *q[NM], *sc[NM];
+#pragma unroll
+  for (int m = 0; m < NM; ++m) {
+    // I % 16 == 0: a tile is whole, or past I (and reads the last one again)
+    const uint64_t row = ((uint64_t)e * 2 + m / RT) * I + min(r0 + m % RT * 16, I - 16) + l16;
+    q[m] = p.gu_q + row * (K / 2);
+    sc[m] = p.gu_s + row * (K / 16);
+  }
   const float g = p.gu_g[e];
   for (uint32_t t0 = 0; t0 < total; t0 += N) {
-    if (t0 > 0) find_tokens(ids, p.S, e, t0, N, list, &first);
+    if (t0 > 0) find_tokens(p.ids, p.S, e, t0, N, list, &first);
     const uint32_t cnt = min(total - t0, N);
-    const uint16_t *x[NT];
-    bool in[NT];
+    ColumnData x[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const Column<PX> c(list, i, cnt);
-      in[i] = c.in;
-      x[i] = p.xs + (int64_t)(l16 / TP) * p.x_plane + (int64_t)(c.slot / p.k) * p.x_ld;
+      x[i].row = p.xp + ((int64_t)(l16 / TP) * p.T + c.slot / p.k) * K;
+      x[i].in = c.in;
     }
-    float4v ag[NT], au[NT];
+    float4v acc[NM][NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) ag[i] = au[i] = (float4v){0, 0, 0, 0};
-    for (uint32_t k0 = wave * CH; k0 < K; k0 += NW * CH) {
-      const uint32_t k = k0 + lq * 64;
-      const bool whole = k0 + CH <= K;
-      const Codes cg = load_codes<ALIGNED>(gq, gs, k, K, whole), cu = load_codes<ALIGNED>(uq, us, k, K, whole);
-      bf16x8 f[NT][8];
+    for (int m = 0; m < NM; ++m)
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = load_column(x[i], in[i], k, K, j);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bf16x8 wg = weights(cg, j), wu = weights(cu, j);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          ag[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wg, f[i][j], ag[i], 0, 0, 0);
-          au[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wu, f[i][j], au[i], 0, 0, 0);
-        }
-      }
-    }
+      for (int i = 0; i < NT; ++i) acc[m][i] = (float4v){0, 0, 0, 0};
+    products<NM, NT, ALIGNED, false>(q, sc, x, K, wave * CH, NW * CH, acc);
     __syncthreads();  // the last pass's sums have been read
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      *reinterpret_cast<float4v *>(&red[wave][0][i * 16 + l16][4 * lq]) = ag[i];
-      *reinterpret_cast<float4v *>(&red[wave][1][i * 16 + l16][4 * lq]) = au[i];
-    }
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) *reinterpret_cast<float4v *>(&red[wave][m][i * 16 + l16][4 * lq]) = acc[m][i];
     __syncthreads();
-    for (uint32_t c = tid / 16; c < cnt; c += 16) {
-      const uint32_t r = tid % 16;
+    for (uint32_t c = tid / (16 * RT); c < cnt; c += 16 / RT) {
+      const uint32_t r = tid % 16, rt = tid / 16 % RT;
+      if (r0 + rt * 16 >= I) continue;
       float zg = 0.0f, zu = 0.0f;
 #pragma unroll
       for (int pl = 0; pl < PX; ++pl)
 #pragma unroll
         for (uint32_t w = 0; w < NW; ++w) {
           const uint32_t col = c / TP * 16 + pl * TP + c % TP;
-          zg += red[w][0][col][r];
-          zu += red[w][1][col][r];
+          zg += red[w][rt][col][r];
+          zu += red[w][RT + rt][col][r];
         }
-      uint16_t o[PH];
-      split<PH>(silu(zg * g) * (zu * g), o);
+      const uint32_t slot = list[c];
+      const int32_t xe = p.xe[slot / p.k];
+      const float h = silu(__builtin_ldexpf(zg * g, xe)) * __builtin_ldexpf(zu * g, xe);
+      // the 16 rows are a row of 16 lanes: their power is one exchange away
+      float top = fabsf(h);
+      top = dpp_max<0x121>(top);
+      top = dpp_max<0x122>(top);
+      top = dpp_max<0x124>(top);
+      top = dpp_max<0x128>(top);
+      const int32_t he = power_of(top);
+      _Float16 o[PH];
+      split<PH>(__builtin_ldexpf(h, -he), o);
 #pragma unroll
-      for (int pl = 0; pl < PH; ++pl) p.h[((int64_t)pl * p.S + list[c]) * I + r0 + r] = o[pl];
+      for (int pl = 0; pl < PH; ++pl) p.h[((int64_t)pl * p.S + slot) * I + r0 + rt * 16 + r] = o[pl];
+      if (r == 0) p.he[(int64_t)slot * p.he_ld + r0 / 16 + rt] = (int8_t)he;
     }
   }
+}
+
+// the largest of a row's n powers (lane quarters take 16 at a time in turn)
+__device__ __forceinline__ int32_t top_power(const int8_t *powers, bool in, uint32_t n) {
+  int32_t top = kNoPower;
+  const uint32_t lq = (threadIdx.x % 64) / 16;
+  for (uint32_t b = lq * 16; b < n; b += 64) {
+    u32x4 w = {0, 0, 0, 0};
+    if (in) w = *reinterpret_cast<const u32x4 *>(powers + b);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (in && b + i < n) top = max(top, (int32_t)(int8_t)(w[i / 4] >> (8 * (i % 4))));
+  }
+  top = max(top, __shfl_xor(top, 16, 64));
+  return max(top, __shfl_xor(top, 32, 64));
 }
 
 // the planes of a token side by side
@@ -412,63 +477,61 @@ __device__ __forceinline__ float4v join_planes(float4v v) {
   return o;
 }
 
-// y[slot][H] = w (Wd h), 64 rows of one expert: a wave per 16
-template <int PH, int NT, bool ALIGNED>
+// y[slot][H] = w (Wd h), 64 RT rows of one expert: a wave per 16 RT
+template <int PH, int NT, int RT, bool ALIGNED>
 __global__ __launch_bounds__(256) void decode_down_kernel(MoeDecodeParams p) {
   constexpr uint32_t TP = kTokens<PH>, N = NT * TP, NW = 4;
   __shared__ uint32_t lists[NW][N];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
   const uint32_t l16 = lane % 16, lq = lane / 16;
-  const uint32_t item = blockIdx.x / p.tiles_h, r0 = (blockIdx.x % p.tiles_h) * 64 + wave * 16;
+  const uint32_t item = blockIdx.x / p.tiles_h, r0 = (blockIdx.x % p.tiles_h) * (64 * RT) + wave * (16 * RT);
   const uint32_t K = p.I, H = p.H;
-  if (r0 >= H) return;  // H % 16 == 0: a wave's rows are all in or all out; no barriers below
+  if (r0 >= H) return;  // no barriers below
   const int32_t e = __builtin_amdgcn_readfirstlane(p.S <= p.E ? p.ids[item] : (int32_t)item);
   uint32_t *list = lists[wave];
   uint32_t first;
   const uint32_t total = find_tokens(p.ids, p.S, e, 0, N, list, &first);
   if (total == 0 || (p.S <= p.E && first != item)) return;
-  const uint64_t row = (uint64_t)e * H + r0 + l16;
-  const uint8_t *dq = p.d_q + row * (K / 2), *ds = p.d_s + row * (K / 16);
+  const uint8_t *q[RT], *sc[RT];
+#pragma unroll
+  for (int m = 0; m < RT; ++m) {
+    // H % 16 == 0: a tile is whole, or past H (and reads the last one again)
+    const uint64_t row = (uint64_t)e * H + min(r0 + m * 16, H - 16) + l16;
+    q[m] = p.d_q + row * (K / 2);
+    sc[m] = p.d_s + row * (K / 16);
+  }
   const float g = p.d_g[e];
   for (uint32_t t0 = 0; t0 < total; t0 += N) {
     if (t0 > 0) find_tokens(p.ids, p.S, e, t0, N, list, &first);
     const uint32_t cnt = min(total - t0, N);
-    const uint16_t *h[NT];
-    bool in[NT];
+    ColumnData h[NT];
     uint32_t slot[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const Column<PH> c(list, i, cnt);
-      in[i] = c.in;
       slot[i] = c.slot;
-      h[i] = p.h + ((int64_t)(l16 / TP) * p.S + c.slot) * K;
+      h[i].row = p.h + ((int64_t)(l16 / TP) * p.S + c.slot) * K;
+      h[i].powers = p.he + (int64_t)c.slot * p.he_ld;
+      h[i].in = c.in;
+      h[i].top = top_power(h[i].powers, c.in, K / 16);
     }
-    float4v acc[NT];
+    float4v acc[RT][NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = (float4v){0, 0, 0, 0};
-    for (uint32_t k0 = 0; k0 < K; k0 += CH) {
-      const uint32_t k = k0 + lq * 64;
-      const Codes cd = load_codes<ALIGNED>(dq, ds, k, K, k0 + CH <= K);
-      bf16x8 f[NT][8];
+    for (int m = 0; m < RT; ++m)
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = load_column(h[i], in[i], k, K, j);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bf16x8 w = weights(cd, j);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, f[i][j], acc[i], 0, 0, 0);
-      }
-    }
+      for (int i = 0; i < NT; ++i) acc[m][i] = (float4v){0, 0, 0, 0};
+    products<RT, NT, ALIGNED, true>(q, sc, h, K, 0, CH, acc);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      float4v v = join_planes<PH>(acc[i]);
-      if (l16 < TP && in[i]) {  // plane 0
-        const float f = g * p.w[slot[i]];
+      const float f = h[i].in ? g * p.w[slot[i]] : 0.0f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] *= f;
-        *reinterpret_cast<float4v *>(p.y + (int64_t)slot[i] * H + r0 + 4 * lq) = v;
+      for (int m = 0; m < RT; ++m) {
+        float4v v = join_planes<PH>(acc[m][i]);
+        if (l16 < TP && h[i].in && r0 + m * 16 < H) {  // plane 0
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = __builtin_ldexpf(v[r] * f, h[i].top);
+          *reinterpret_cast<float4v *>(p.y + (int64_t)slot[i] * H + r0 + m * 16 + 4 * lq) = v;
+        }
       }
     }
   }
@@ -518,24 +581,20 @@ __global__ __launch_bounds__(1024) void decode_own_kernel(MoeDecodeParams p) {
     const uint64_t row = (uint64_t)e * H + r0 + l16;
     const uint8_t *dq = p.d_q + row * (K / 2), *ds = p.d_s + row * (K / 16);
     const float fac = p.d_g[e] * p.w[slot];
-    const bool in = l16 % TP == 0 && l16 / TP < (uint32_t)PH;
-    const uint16_t *h = p.h + ((int64_t)(l16 / TP) * p.S + slot) * K;
-    float4v acc = {0, 0, 0, 0};
-    for (uint32_t k0 = part * CH; k0 < K; k0 += parts * CH) {
-      const uint32_t k = k0 + lq * 64;
-      const Codes cd = load_codes<ALIGNED>(dq, ds, k, K, k0 + CH <= K);
-      bf16x8 f[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = load_column(h, in, k, K, j);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(weights(cd, j), f[j], acc, 0, 0, 0);
-    }
-    acc = join_planes<PH>(acc);
+    ColumnData h[1];
+    h[0].in = l16 % TP == 0;  // a column for each plane
+    h[0].row = p.h + ((int64_t)(l16 / TP) * p.S + slot) * K;
+    h[0].powers = p.he + (int64_t)slot * p.he_ld;
+    h[0].top = top_power(h[0].powers, h[0].in, K / 16);
+    const uint8_t *const q[1] = {dq}, *const sc[1] = {ds};
+    float4v a[1][1] = {{{0, 0, 0, 0}}};
+    products<1, 1, ALIGNED, true>(q, sc, h, K, part * CH, parts * CH, a);
+    const float4v acc = join_planes<PH>(a[0][0]);
     if (l16 == 0) {
       float4v *at = reinterpret_cast<float4v *>(&sum[wave][slot / p.k][4 * lq]);
       float4v v = *at;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] += acc[r] * fac;
+      for (int r = 0; r < 4; ++r) v[r] += __builtin_ldexpf(acc[r] * fac, h[0].top);
       *at = v;
     }
   }
@@ -559,19 +618,33 @@ int column_tiles(const MoeDecodeParams &p) {
   return mean * 2 <= kTokens<P> ? 1 : mean <= kTokens<P> ? 2 : 4;
 }
 
-template <int PX, int PH, bool ALIGNED>
-void launch_gate_up(const MoeDecodeParams &p, bool fuse, hipStream_t stream) {
+// Row tiles: two (gate_up) and four (down) a wave keep twice and four times the
+// bytes in flight and read the columns as much less often; one while there are few
+// workgroups.
+template <int PX, int PH, int RT, bool ALIGNED>
+void launch_gate_up_rt(MoeDecodeParams p, hipStream_t stream) {
+  p.tiles_i = (p.I + 16 * RT - 1) / (16 * RT);
   const uint32_t grid = p.tiles_i * min(p.S, p.E);
-  if constexpr (PX == 1) {
-    if (fuse) {
-      decode_gate_up_kernel<PX, PH, 1, ALIGNED, true><<<grid, 256, 0, stream>>>(p);
-      return;
-    }
-  }
   const int nt = column_tiles<PX>(p);
-  if (nt == 1) decode_gate_up_kernel<PX, PH, 1, ALIGNED, false><<<grid, 256, 0, stream>>>(p);
-  else if (nt == 2) decode_gate_up_kernel<PX, PH, 2, ALIGNED, false><<<grid, 256, 0, stream>>>(p);
-  else decode_gate_up_kernel<PX, PH, 4, ALIGNED, false><<<grid, 256, 0, stream>>>(p);
+  if (nt == 1) decode_gate_up_kernel<PX, PH, 1, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
+  else if (nt == 2) decode_gate_up_kernel<PX, PH, 2, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
+  else decode_gate_up_kernel<PX, PH, 4, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
+}
+
+template <int PX, int PH, bool ALIGNED>
+void launch_gate_up(const MoeDecodeParams &p, hipStream_t stream) {
+  if ((uint64_t)(p.I / 16) * min(p.S, p.E) >= RTG_MIN * device_cu_count()) launch_gate_up_rt<PX, PH, 2, ALIGNED>(p, stream);
+  else launch_gate_up_rt<PX, PH, 1, ALIGNED>(p, stream);
+}
+
+template <int PH, int RT, bool ALIGNED>
+void launch_down_rt(MoeDecodeParams p, hipStream_t stream) {
+  p.tiles_h = (p.H + 64 * RT - 1) / (64 * RT);
+  const uint32_t grid = p.tiles_h * min(p.S, p.E);
+  const int nt = column_tiles<PH>(p);
+  if (nt == 1) decode_down_kernel<PH, 1, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
+  else if (nt == 2) decode_down_kernel<PH, 2, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
+  else decode_down_kernel<PH, 4, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
 }
 
 template <int PH, bool ALIGNED, typename OutT>
@@ -580,11 +653,8 @@ hipError_t launch_down(const MoeDecodeParams &p, hipStream_t stream) {
     decode_own_kernel<PH, ALIGNED, OutT><<<p.H / 16, 1024, 0, stream>>>(p);
     return hipGetLastError();
   }
-  const uint32_t grid = p.tiles_h * min(p.S, p.E);
-  const int nt = column_tiles<PH>(p);
-  if (nt == 1) decode_down_kernel<PH, 1, ALIGNED><<<grid, 256, 0, stream>>>(p);
-  else if (nt == 2) decode_down_kernel<PH, 2, ALIGNED><<<grid, 256, 0, stream>>>(p);
-  else decode_down_kernel<PH, 4, ALIGNED><<<grid, 256, 0, stream>>>(p);
+  if ((uint64_t)(p.H / 64) * min(p.S, p.E) >= RTD_MIN * device_cu_count()) launch_down_rt<PH, 4, ALIGNED>(p, stream);
+  else launch_down_rt<PH, 1, ALIGNED>(p, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   decode_combine_kernel<OutT><<<dim3((p.H + 1023) / 1024, p.T), 256, 0, stream>>>(p);
@@ -592,9 +662,9 @@ hipError_t launch_down(const MoeDecodeParams &p, hipStream_t stream) {
 }
 
 template <int PX, int PH, typename OutT>
-hipError_t launch_products(const MoeDecodeParams &p, bool fuse, bool gu_aligned, bool d_aligned, hipStream_t stream) {
-  if (gu_aligned) launch_gate_up<PX, PH, true>(p, fuse, stream);
-  else launch_gate_up<PX, PH, false>(p, fuse, stream);
+hipError_t launch_products(const MoeDecodeParams &p, bool gu_aligned, bool d_aligned, hipStream_t stream) {
+  if (gu_aligned) launch_gate_up<PX, PH, true>(p, stream);
+  else launch_gate_up<PX, PH, false>(p, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   return d_aligned ? launch_down<PH, true, OutT>(p, stream) : launch_down<PH, false, OutT>(p, stream);
@@ -602,49 +672,60 @@ hipError_t launch_products(const MoeDecodeParams &p, bool fuse, bool gu_aligned,
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
+// the workspace's parts, in order, from its base
+struct DecodeParts {
+  size_t ids, w, xe, xp, h, he, y, total;
+  int64_t he_ld;
+  DecodeParts(size_t T, size_t k, size_t H, size_t I) {
+    const size_t S = T * k;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+      const size_t r = at;
+      at += align256(bytes);
+      return r;
+    };
+    he_ld = (int64_t)((I / 16 + 15) / 16 * 16);
+    ids = take(S * 4);
+    w = take(S * 4);
+    xe = take(T * 4);
+    xp = take(2 * T * H * 2);
+    h = take(2 * S * I * 2);
+    he = take(S * (size_t)he_ld);
+    y = take(S * H * 4);
+    total = at;
+  }
+};
+
 }  // namespace
 
 size_t moe_decode_workspace_bytes(int64_t T, int32_t /*E*/, int32_t k, int64_t H, int64_t I) {
-  const size_t S = (size_t)T * k;
-  return 2 * align256(S * 4) + align256(3 * (size_t)T * H * 2) + align256(3 * S * (size_t)I * 2) +
-         align256(S * (size_t)H * 4);
+  return DecodeParts((size_t)T, (size_t)k, (size_t)H, (size_t)I).total;
 }
 
-hipError_t launch_moe_decode(MoeDecodeParams p, bool x_bf16, bool x_vec, bool gu_aligned, bool d_aligned,
-                             bool out_bf16, void *workspace, hipStream_t stream) {
+hipError_t launch_moe_decode(MoeDecodeParams p, bool x_bf16, bool gu_aligned, bool d_aligned, bool out_bf16,
+                             void *workspace, hipStream_t stream) {
   if (p.T == 0) return hipSuccess;
   p.S = p.T * p.k;
-  p.tiles_i = p.I / 16;
-  p.tiles_h = (p.H + 63) / 64;
-  uint8_t *at = static_cast<uint8_t *>(workspace);
-  auto take = [&](size_t bytes) {
-    uint8_t *r = at;
-    at += align256(bytes);
-    return r;
-  };
-  p.ids = reinterpret_cast<int32_t *>(take((size_t)p.S * 4));
-  p.w = reinterpret_cast<float *>(take((size_t)p.S * 4));
-  p.xp = reinterpret_cast<uint16_t *>(take(3 * (size_t)p.T * p.H * 2));
-  p.h = reinterpret_cast<uint16_t *>(take(3 * (size_t)p.S * p.I * 2));
-  p.y = reinterpret_cast<float *>(take((size_t)p.S * p.H * 4));
-  const bool copy = !x_bf16 || !x_vec;
-  p.xs = copy ? p.xp : static_cast<const uint16_t *>(p.x);
-  p.x_ld = copy ? (int64_t)p.H : p.ld_x;
-  p.x_plane = (int64_t)p.T * p.H;
-  const bool fuse = p.T <= kFuseT && !copy;
-  if (!fuse) {
-    p.topk_blocks = (p.T + 3) / 4;
-    const uint32_t grid = p.topk_blocks + (copy ? p.T * ((p.H + 255) / 256) : 0u);
-    if (x_bf16) decode_prep_kernel<1><<<grid, 256, 0, stream>>>(p);
-    else decode_prep_kernel<3><<<grid, 256, 0, stream>>>(p);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
+  uint8_t *const ws = static_cast<uint8_t *>(workspace);
+  const DecodeParts at(p.T, p.k, p.H, p.I);
+  p.ids = reinterpret_cast<int32_t *>(ws + at.ids);
+  p.w = reinterpret_cast<float *>(ws + at.w);
+  p.xe = reinterpret_cast<int32_t *>(ws + at.xe);
+  p.xp = reinterpret_cast<_Float16 *>(ws + at.xp);
+  p.h = reinterpret_cast<_Float16 *>(ws + at.h);
+  p.he = reinterpret_cast<int8_t *>(ws + at.he);
+  p.y = reinterpret_cast<float *>(ws + at.y);
+  p.he_ld = at.he_ld;
+  p.topk_blocks = (p.T + 3) / 4;
+  if (x_bf16) decode_prep_kernel<1><<<p.topk_blocks + p.T, 256, 0, stream>>>(p);
+  else decode_prep_kernel<2><<<p.topk_blocks + p.T, 256, 0, stream>>>(p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   if (x_bf16)
-    return out_bf16 ? launch_products<1, 2, uint16_t>(p, fuse, gu_aligned, d_aligned, stream)
-                    : launch_products<1, 3, float>(p, fuse, gu_aligned, d_aligned, stream);
-  return out_bf16 ? launch_products<3, 2, uint16_t>(p, fuse, gu_aligned, d_aligned, stream)
-                  : launch_products<3, 3, float>(p, fuse, gu_aligned, d_aligned, stream);
+    return out_bf16 ? launch_products<1, 1, uint16_t>(p, gu_aligned, d_aligned, stream)
+                    : launch_products<1, 2, float>(p, gu_aligned, d_aligned, stream);
+  return out_bf16 ? launch_products<2, 1, uint16_t>(p, gu_aligned, d_aligned, stream)
+                  : launch_products<2, 2, float>(p, gu_aligned, d_aligned, stream);
 }
 
 }  // namespace nvfp4

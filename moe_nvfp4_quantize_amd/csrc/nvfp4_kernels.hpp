@@ -152,20 +152,22 @@ struct MoeDecodeParams {
   void *out;
   int64_t ld_out;
 
-  uint32_t S, tiles_i, tiles_h;  // slots T k; 16-row tiles of I; 64-row tiles of H
-  uint32_t topk_blocks;          // workgroups of the prep kernel that route
-  int32_t *ids;                  // [S] expert of slot t k + j
-  float *w;                      // [S] routing weight
-  uint16_t *xp;                  // [3][T][H] bf16 planes of x
-  uint16_t *h;                   // [3][S][I] bf16 planes of h
-  float *y;                      // [S][H] weighted products
-  const uint16_t *xs;            // the rows the products read: x itself or xp
-  int64_t x_ld, x_plane;
+  uint32_t S;                  // slots T k
+  uint32_t tiles_i, tiles_h;   // row tiles of I and H (a launch's own)
+  uint32_t topk_blocks;        // workgroups of the prep kernel that route
+  int32_t *ids;                // [S] expert of slot t k + j
+  float *w;                    // [S] routing weight
+  int32_t *xe;                 // [T] x's power of two
+  _Float16 *xp;                // [2][T][H] f16 planes of x
+  _Float16 *h;                 // [2][S][I] f16 planes of h
+  int8_t *he;                  // [S][he_ld] h's powers, a block of 16 each
+  int64_t he_ld;               // I / 16 rounded up to 16
+  float *y;                    // [S][H] weighted products
 };
 
 constexpr uint32_t kMaxDecodeTokens = 128;
 size_t moe_decode_workspace_bytes(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I);
-hipError_t launch_moe_decode(MoeDecodeParams p, bool x_bf16, bool x_vec, bool gu_aligned, bool d_aligned,
-                             bool out_bf16, void *workspace, hipStream_t stream);
+hipError_t launch_moe_decode(MoeDecodeParams p, bool x_bf16, bool gu_aligned, bool d_aligned, bool out_bf16,
+                             void *workspace, hipStream_t stream);
 
 }  // namespace nvfp4

@@ -1,8 +1,8 @@
 """GPU parity of the few-token routed-expert layer against its oracle.
 
 Every output lies within the bound that the oracle carries through the layer for a float32
-evaluation (h to 18 bits for bf16 outputs), plus half a bf16 step (2^-8 relative at most)
-where the output is bf16.  Routing is the routed call's own, so a wrong expert or weight
+evaluation (h as one f16 value for bf16 outputs, x and h as two otherwise; a bf16 x is exact),
+plus half a bf16 step (2^-8 relative at most) where the output is bf16.  Routing is the routed call's own, so a wrong expert or weight
 shows as a gross error.
 """
 
@@ -40,7 +40,8 @@ def _case(T, E, k, H, I, seed=0):
 def _check(y, x, logits, k, gu, dn):
     bf16 = y.dtype == torch.bfloat16
     ref, tol = OD.forward(x.float().cpu().numpy(), logits.cpu().numpy(), k, [t.cpu().numpy() for t in gu],
-                          [t.cpu().numpy() for t in dn], h_bits=18 if bf16 else 24)
+                          [t.cpu().numpy() for t in dn], x_bits=None if x.dtype == torch.bfloat16 else 22,
+                          h_bits=11 if bf16 else 22)
     if bf16:
         tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
     err = np.abs(y.double().cpu().numpy() - ref)
@@ -103,6 +104,8 @@ def test_ties_extremes_and_shared_experts(B):
     x[11] = 0.0
     x[4] *= 1e4
     x[5] *= 1e-12
+    x[6, ::3] *= 1e-9                     # small beside the row's largest
+    x[7] *= 1e-30
     for dt in (torch.bfloat16, torch.float32):
         y = B.nvfp4_moe_decode(x.to(dt), logits, k, gu, dn, out_dtype=torch.float32)
         _check(y, x.to(dt), logits, k, gu, dn)
