@@ -73,50 +73,36 @@ __device__ __forceinline__ float wave_max_uniform(float v) {
   return u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(v), 63));
 }
 
-// Top-k of one row by one wave: lane l holds logits l * PL .. l * PL + PL - 1, sorted
-// (stable, so equal logits keep the lower id first); each round the wave's largest
-// head wins, equal heads going to the lowest lane, and that lane drops it.  Lane
-// j < k returns the j-th expert and its routing weight.
+// Top-k of one row by one wave: lane l holds logits l * PL .. l * PL + PL - 1, a taken
+// or missing one as NaN (a maximum passes over it; a NaN logit ranks as -infinity).
+// Each round takes the wave's largest: equal logits go to the lowest lane and, in
+// it, to the lowest index, the lower expert id.  Lane j < k returns the j-th expert
+// and its routing weight.
 template <int PL>
 __device__ __forceinline__ void topk_row(const float *row, uint32_t E, uint32_t k, int32_t *id, float *w) {
   const uint32_t lane = threadIdx.x % 64;
   float v[PL];
-  int32_t x[PL];  // index inside the lane; 64: no logit (sorted last, never taken: k <= E)
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     const uint32_t e = lane * PL + i;
-    v[i] = e < E ? router_logit(row[e]) : -INFINITY;
-    x[i] = e < E ? i : 64;
+    v[i] = e < E ? router_logit(row[e]) : __builtin_nanf("");
   }
-  // odd-even transposition: neighbours only, so equal logits never pass each other
-#pragma unroll
-  for (int r = 0; r < PL; ++r)
-#pragma unroll
-    for (int i = r % 2; i + 1 < PL; i += 2) {
-      const bool sw = topk_before(v[i + 1], x[i + 1], v[i], x[i]);
-      const float a = v[i], b = v[i + 1];
-      const int32_t c = x[i], d = x[i + 1];
-      v[i] = sw ? b : a;
-      v[i + 1] = sw ? a : b;
-      x[i] = sw ? d : c;
-      x[i + 1] = sw ? c : d;
-    }
   float sel_v = 0.0f;
   int32_t sel_e = 0;
   for (uint32_t j = 0; j < k; ++j) {
-    const float top = wave_max_uniform(v[0]);
-    const unsigned long long at = __ballot(x[0] < 64 && v[0] == top);
-    const uint32_t win = (uint32_t)__builtin_ctzll(at);
-    const int32_t wi = __builtin_amdgcn_readlane(x[0], win);
-    if (lane == win) {
+    float m = v[0];
 #pragma unroll
-      for (int i = 0; i + 1 < PL; ++i) {
-        v[i] = v[i + 1];
-        x[i] = x[i + 1];
-      }
-      v[PL - 1] = -INFINITY;
-      x[PL - 1] = 64;
-    }
+    for (int i = 1; i < PL; ++i) m = fmaxf(m, v[i]);
+    const float top = wave_max_uniform(m);
+    // k <= E: some lane still has a logit, and a NaN equals nothing
+    const uint32_t win = (uint32_t)__builtin_ctzll(__ballot(m == top));
+    int32_t at = 0;
+#pragma unroll
+    for (int i = PL - 1; i >= 0; --i) at = v[i] == top ? i : at;
+    const int32_t wi = __builtin_amdgcn_readlane(at, win);
+    const int32_t gone = lane == win ? wi : -1;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) v[i] = i == gone ? __builtin_nanf("") : v[i];
     if (lane == j) {
       sel_v = top;
       sel_e = (int32_t)(win * PL) + wi;
@@ -166,35 +152,62 @@ __global__ __launch_bounds__(256) void decode_prep_kernel(MoeDecodeParams p) {
     }
     return;
   }
+  // eight elements a thread and turn (H % 16 == 0); rows up to 4096 stay in registers
   const uint32_t t = blockIdx.x - p.topk_blocks;
-  auto load = [&](uint32_t h) {
-    if constexpr (P == 1) return u2f((uint32_t)((const uint16_t *)p.x)[(int64_t)t * p.ld_x + h] << 16);
-    else return ((const float *)p.x)[(int64_t)t * p.ld_x + h];
+  auto load = [&](uint32_t h, float v[8]) {
+    if constexpr (P == 1) {
+      u32x4 w;
+      __builtin_memcpy(&w, (const uint16_t *)p.x + (int64_t)t * p.ld_x + h, 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+      }
+    } else {
+      __builtin_memcpy(v, (const float *)p.x + (int64_t)t * p.ld_x + h, 32);
+    }
   };
-  constexpr int U = 16;  // elements a thread keeps: rows up to 4096 are read once
-  float v[U];
+  auto largest = [](const float v[8], float m) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    return m;
+  };
+  constexpr uint32_t U = 2, TURN = 256 * 8;
+  const uint32_t h0 = threadIdx.x * 8;
+  float v[U][8] = {};
+#pragma unroll
+  for (uint32_t i = 0; i < U; ++i)
+    if (h0 + i * TURN < p.H) load(h0 + i * TURN, v[i]);
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const uint32_t h = i * 256 + threadIdx.x;
-    v[i] = h < p.H ? load(h) : 0.0f;
-    m = fmaxf(m, fabsf(v[i]));
+  for (uint32_t i = 0; i < U; ++i) m = largest(v[i], m);
+  for (uint32_t h = h0 + U * TURN; h < p.H; h += TURN) {
+    float x[8];
+    load(h, x);
+    m = largest(x, m);
   }
-  for (uint32_t h = U * 256 + threadIdx.x; h < p.H; h += 256) m = fmaxf(m, fabsf(load(h)));
   const int32_t e = power_of(block_max(m));
   if (threadIdx.x == 0) p.xe[t] = e;
-  auto store = [&](uint32_t h, float x) {
-    _Float16 o[P];
-    split<P>(__builtin_ldexpf(x, -e), o);
+  auto store = [&](uint32_t h, const float x[8]) {
+    _Float16 o[8][P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) p.xp[((int64_t)i * p.T + t) * p.H + h] = o[i];
+    for (int i = 0; i < 8; ++i) split<P>(__builtin_ldexpf(x[i], -e), o[i]);
+#pragma unroll
+    for (int pl = 0; pl < P; ++pl) {
+      half8v w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = o[i][pl];
+      *reinterpret_cast<half8v *>(p.xp + ((int64_t)pl * p.T + t) * p.H + h) = w;
+    }
   };
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const uint32_t h = i * 256 + threadIdx.x;
-    if (h < p.H) store(h, v[i]);
+  for (uint32_t i = 0; i < U; ++i)
+    if (h0 + i * TURN < p.H) store(h0 + i * TURN, v[i]);
+  for (uint32_t h = h0 + U * TURN; h < p.H; h += TURN) {
+    float x[8];
+    load(h, x);
+    store(h, x);
   }
-  for (uint32_t h = U * 256 + threadIdx.x; h < p.H; h += 256) store(h, load(h));
 }
 
 // ---------------------------------------------------------------- products
@@ -539,12 +552,12 @@ __global__ __launch_bounds__(256) void decode_down_kernel(MoeDecodeParams p) {
 
 // out[t] = the sum of its slots' rows, in slot order; H % 16 == 0: four columns a thread
 template <typename OutT>
-__global__ __launch_bounds__(256) void decode_combine_kernel(MoeDecodeParams p) {
-  const uint32_t h = (blockIdx.x * 256 + threadIdx.x) * 4, t = blockIdx.y;
+__global__ __launch_bounds__(64) void decode_combine_kernel(MoeDecodeParams p) {
+  const uint32_t h = (blockIdx.x * 64 + threadIdx.x) * 4, t = blockIdx.y;
   if (h >= p.H) return;
   const float *y = p.y + (int64_t)t * p.k * p.H + h;
   float4v v = {0, 0, 0, 0};
-#pragma unroll 4
+#pragma unroll 8
   for (uint32_t j = 0; j < p.k; ++j) {
     const float4v o = *reinterpret_cast<const float4v *>(y + (int64_t)j * p.H);
 #pragma unroll
@@ -657,7 +670,7 @@ hipError_t launch_down(const MoeDecodeParams &p, hipStream_t stream) {
   else launch_down_rt<PH, 1, ALIGNED>(p, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  decode_combine_kernel<OutT><<<dim3((p.H + 1023) / 1024, p.T), 256, 0, stream>>>(p);
+  decode_combine_kernel<OutT><<<dim3((p.H + 255) / 256, p.T), 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 

@@ -147,15 +147,21 @@ def _one_device(*ts):
     return dev
 
 
+# the handle of a device's current stream, without the Stream object around it
+# (2.8 us of a small call's 12)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on_stream(device, stream, body):
     """body(raw stream) with ``device`` current and ``stream`` (default: the
     device's current one) as its current stream: what it allocates belongs to
     the stream that its kernels run on."""
     if stream is None and torch.cuda.current_device() == device.index:
-        return body(torch.cuda.current_stream().cuda_stream)
+        return body(_raw_stream(device.index))
     with torch.cuda.device(device):
         if stream is None:
-            return body(torch.cuda.current_stream().cuda_stream)
+            return body(_raw_stream(device.index))
         if stream.device != device:
             raise ValueError("stream and tensors are on different GPUs")
         with torch.cuda.stream(stream):
