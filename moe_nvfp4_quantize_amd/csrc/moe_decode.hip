@@ -280,7 +280,7 @@ __device__ __forceinline__ half8v weights(const Codes &c, int j) {
 }
 
 // A lane's column in column tile i: its row of f16 values, and, for h, the powers
-// of its blocks of 16 and their largest.
+// of its blocks of 16 and the power that the sums are under so far.
 struct ColumnData {
   const _Float16 *row;
   const int8_t *powers;
@@ -289,11 +289,11 @@ struct ColumnData {
 };
 
 // acc[m][i] += 16 rows of matrix m x column tile i, over the steps k0 = first, first +
-// turn, ... of 256 each.  POWERS: each block of the column is brought to its row's
-// largest power.
+// turn, ... of 256 each.  POWERS: each block of the column is brought to the largest
+// power met so far, the sums with it (as a running maximum carries a softmax).
 template <int NM, int NT, bool ALIGNED, bool POWERS>
 __device__ __forceinline__ void products(const uint8_t *const (&q)[NM], const uint8_t *const (&s)[NM],
-                                         const ColumnData (&x)[NT], uint32_t K, uint32_t first, uint32_t turn,
+                                         ColumnData (&x)[NT], uint32_t K, uint32_t first, uint32_t turn,
                                          float4v (&acc)[NM][NT]) {
   const uint32_t kq = (threadIdx.x % 64) / 16 * 64;
   for (uint32_t k0 = first; k0 < K; k0 += turn) {
@@ -311,12 +311,24 @@ __device__ __forceinline__ void products(const uint8_t *const (&q)[NM], const ui
         f[i][j] = __builtin_bit_cast(half8v, v);
       }
       if constexpr (POWERS) {
-        // a row of powers is padded to 16 bytes, so the four of 64 elements are one load
-        const uint32_t w = x[i].in && k < K ? *reinterpret_cast<const uint32_t *>(x[i].powers + k / 16) : 0u;
+        // a row of powers is padded to 4 bytes, so the four of 64 elements are one load
+        const uint32_t w = x[i].in && k < K ? *reinterpret_cast<const uint32_t *>(x[i].powers + k / 16) : 0x80808080u;
+        int32_t e[4], top = x[i].top;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const int32_t d = min((int32_t)(int8_t)(w >> (8 * b)) - x[i].top, 0);  // (blocks past K: anything)
-          const _Float16 h = __builtin_amdgcn_ldexph((_Float16)1.0f, d);  // 0 below 2^-24
+          e[b] = k + 16 * b < K ? (int32_t)(int8_t)(w >> (8 * b)) : kNoPower;
+          top = max(top, e[b]);
+        }
+        top = max(top, __shfl_xor(top, 16, 64));  // the column's other quarters
+        top = max(top, __shfl_xor(top, 32, 64));
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[m][i][r] = __builtin_ldexpf(acc[m][i][r], x[i].top - top);
+        x[i].top = top;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const _Float16 h = __builtin_amdgcn_ldexph((_Float16)1.0f, e[b] - top);  // 0 below 2^-24
 #pragma unroll
           for (int j = 2 * b; j < 2 * b + 2; ++j) f[i][j] *= (half8v){h, h, h, h, h, h, h, h};
         }
@@ -355,6 +367,7 @@ __device__ __forceinline__ uint32_t find_tokens(const int32_t *ids, uint32_t S, 
     for (int i = 0; i < 8; ++i) id[i] = s0 + i * 64 + lane < S ? ids[s0 + i * 64 + lane] : -1;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      if (s0 + i * 64 >= S) break;
       const unsigned long long m = __ballot(id[i] == e);
       if (m == 0) continue;
       const uint32_t s = s0 + i * 64 + lane;
@@ -463,21 +476,6 @@ __global__ __launch_bounds__(256) void decode_gate_up_kernel(MoeDecodeParams p) 
   }
 }
 
-// the largest of a row's n powers (lane quarters take 16 at a time in turn)
-__device__ __forceinline__ int32_t top_power(const int8_t *powers, bool in, uint32_t n) {
-  int32_t top = kNoPower;
-  const uint32_t lq = (threadIdx.x % 64) / 16;
-  for (uint32_t b = lq * 16; b < n; b += 64) {
-    u32x4 w = {0, 0, 0, 0};
-    if (in) w = *reinterpret_cast<const u32x4 *>(powers + b);
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (in && b + i < n) top = max(top, (int32_t)(int8_t)(w[i / 4] >> (8 * (i % 4))));
-  }
-  top = max(top, __shfl_xor(top, 16, 64));
-  return max(top, __shfl_xor(top, 32, 64));
-}
-
 // the planes of a token side by side
 template <int PH>
 __device__ __forceinline__ float4v join_planes(float4v v) {
@@ -526,7 +524,7 @@ __global__ __launch_bounds__(256) void decode_down_kernel(MoeDecodeParams p) {
       h[i].row = p.h + ((int64_t)(l16 / TP) * p.S + c.slot) * K;
       h[i].powers = p.he + (int64_t)c.slot * p.he_ld;
       h[i].in = c.in;
-      h[i].top = top_power(h[i].powers, c.in, K / 16);
+      h[i].top = kNoPower;
     }
     float4v acc[RT][NT];
 #pragma unroll
@@ -598,7 +596,7 @@ __global__ __launch_bounds__(1024) void decode_own_kernel(MoeDecodeParams p) {
     h[0].in = l16 % TP == 0;  // a column for each plane
     h[0].row = p.h + ((int64_t)(l16 / TP) * p.S + slot) * K;
     h[0].powers = p.he + (int64_t)slot * p.he_ld;
-    h[0].top = top_power(h[0].powers, h[0].in, K / 16);
+    h[0].top = kNoPower;
     const uint8_t *const q[1] = {dq}, *const sc[1] = {ds};
     float4v a[1][1] = {{{0, 0, 0, 0}}};
     products<1, 1, ALIGNED, true>(q, sc, h, K, part * CH, parts * CH, a);
@@ -697,7 +695,7 @@ struct DecodeParts {
       at += align256(bytes);
       return r;
     };
-    he_ld = (int64_t)((I / 16 + 15) / 16 * 16);
+    he_ld = (int64_t)((I / 16 + 3) / 4 * 4);
     ids = take(S * 4);
     w = take(S * 4);
     xe = take(T * 4);

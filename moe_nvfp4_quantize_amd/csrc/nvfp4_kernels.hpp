@@ -161,7 +161,7 @@ struct MoeDecodeParams {
   _Float16 *xp;                // [2][T][H] f16 planes of x
   _Float16 *h;                 // [2][S][I] f16 planes of h
   int8_t *he;                  // [S][he_ld] h's powers, a block of 16 each
-  int64_t he_ld;               // I / 16 rounded up to 16
+  int64_t he_ld;               // I / 16 rounded up to 4
   float *y;                    // [S][H] weighted products
 };
 
