@@ -50,10 +50,6 @@ typedef _Float16 half8v __attribute__((ext_vector_type(8)));
 
 constexpr int CH = 256;  // K elements per wave step: 64 per lane quarter
 
-#ifndef RTG_MIN
-#define RTG_MIN 4
-#define RTD_MIN 8
-#endif
 // ------------------------------------------------------------------- route
 
 // maximum over the wave, in every lane (scalar): rows of 16 by rotations, then
@@ -226,28 +222,22 @@ __device__ __forceinline__ half8v decode8(uint32_t w, _Float16 s) {
 
 // What a lane holds of 16 weight rows for one 256-wide step: 64 codes of its row
 // and their 4 block scales.
+// Swizzle of the eight 16-byte pieces of a 128-byte LDS row (fp8_block_gemm.hip)
+__device__ __forceinline__ uint32_t swz128(uint32_t r) { return (r >> 1) & 7u; }
+
 struct Codes {
   u32x4 lo, hi;
   uint32_t s;
 };
 
-// A lane's 64 elements [k, k + 64) of its row.
-//  ALIGNED (K % 64 == 0, 16-byte aligned codes, 4-byte aligned scales): all in or
-//  all out.  Otherwise a whole step (all lanes in) takes the same loads at whatever
-//  alignment the row has, and the last step goes block by block of 16, each all in
-//  or all out (K % 16 == 0).
-template <bool ALIGNED>
+// A lane's 64 elements [k, k + 64) of its row, at whatever alignment the row has: a
+// whole step (every lane in) by wide loads, the last one block by block of 16, each
+// all in or all out (K % 16 == 0).
 __device__ __forceinline__ Codes load_codes(const uint8_t *q, const uint8_t *s, uint32_t k, uint32_t K, bool whole) {
   Codes c;
   c.lo = c.hi = (u32x4){0, 0, 0, 0};
   c.s = 0;
-  if constexpr (ALIGNED) {
-    if (k < K) {
-      c.lo = *reinterpret_cast<const u32x4 *>(q + k / 2);
-      c.hi = *reinterpret_cast<const u32x4 *>(q + k / 2 + 16);
-      c.s = *reinterpret_cast<const uint32_t *>(s + k / 16);
-    }
-  } else if (whole) {
+  if (whole) {
     __builtin_memcpy(&c.lo, q + k / 2, 16);
     __builtin_memcpy(&c.hi, q + k / 2 + 16, 16);
     __builtin_memcpy(&c.s, s + k / 16, 4);
@@ -288,20 +278,12 @@ struct ColumnData {
   bool in;
 };
 
-// acc[m][i] += 16 rows of matrix m x column tile i, over the steps k0 = first, first +
-// turn, ... of 256 each.  POWERS: each block of the column is brought to the largest
-// power met so far, the sums with it (as a running maximum carries a softmax).
-template <int NM, int NT, bool ALIGNED, bool POWERS>
-__device__ __forceinline__ void products(const uint8_t *const (&q)[NM], const uint8_t *const (&s)[NM],
-                                         ColumnData (&x)[NT], uint32_t K, uint32_t first, uint32_t turn,
-                                         float4v (&acc)[NM][NT]) {
-  const uint32_t kq = (threadIdx.x % 64) / 16 * 64;
-  for (uint32_t k0 = first; k0 < K; k0 += turn) {
-    const uint32_t k = k0 + kq;
-    Codes c[NM];
-#pragma unroll
-    for (int m = 0; m < NM; ++m) c[m] = load_codes<ALIGNED>(q[m], s[m], k, K, k0 + CH <= K);
-    half8v f[NT][8];
+// A step's columns: the fragments of 256 elements from k0 and, for h, their powers.
+template <int NT, bool POWERS>
+struct Columns {
+  half8v f[NT][8];
+  uint32_t w[NT];
+  __device__ __forceinline__ void load(const ColumnData (&x)[NT], uint32_t k, uint32_t K) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -310,38 +292,189 @@ __device__ __forceinline__ void products(const uint8_t *const (&q)[NM], const ui
         if (x[i].in && k + 8 * j < K) v = *reinterpret_cast<const u32x4 *>(x[i].row + k + 8 * j);
         f[i][j] = __builtin_bit_cast(half8v, v);
       }
-      if constexpr (POWERS) {
-        // a row of powers is padded to 4 bytes, so the four of 64 elements are one load
-        const uint32_t w = x[i].in && k < K ? *reinterpret_cast<const uint32_t *>(x[i].powers + k / 16) : 0x80808080u;
-        int32_t e[4], top = x[i].top;
+      if constexpr (POWERS) load_powers(x[i], i, k, K);
+    }
+  }
+  // a row of powers is padded to 4 bytes, so the four of 64 elements are one load
+  __device__ __forceinline__ void load_powers(const ColumnData &x, int i, uint32_t k, uint32_t K) {
+    w[i] = x.in && k < K ? *reinterpret_cast<const uint32_t *>(x.powers + k / 16) : 0x80808080u;
+  }
+  // each block to the largest power met so far, the sums with it (as a running
+  // maximum carries a softmax)
+  template <int NM>
+  __device__ __forceinline__ void align(ColumnData (&x)[NT], uint32_t k, uint32_t K, float4v (&acc)[NM][NT]) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          e[b] = k + 16 * b < K ? (int32_t)(int8_t)(w >> (8 * b)) : kNoPower;
-          top = max(top, e[b]);
-        }
-        top = max(top, __shfl_xor(top, 16, 64));  // the column's other quarters
-        top = max(top, __shfl_xor(top, 32, 64));
+    for (int i = 0; i < NT; ++i) {
+      int32_t e[4], top = x[i].top;
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
+      for (int b = 0; b < 4; ++b) {
+        e[b] = k + 16 * b < K ? (int32_t)(int8_t)(w[i] >> (8 * b)) : kNoPower;
+        top = max(top, e[b]);
+      }
+      top = max(top, __shfl_xor(top, 16, 64));  // the column's other quarters
+      top = max(top, __shfl_xor(top, 32, 64));
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[m][i][r] = __builtin_ldexpf(acc[m][i][r], x[i].top - top);
-        x[i].top = top;
+      for (int m = 0; m < NM; ++m)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const _Float16 h = __builtin_amdgcn_ldexph((_Float16)1.0f, e[b] - top);  // 0 below 2^-24
+        for (int r = 0; r < 4; ++r) acc[m][i][r] = __builtin_ldexpf(acc[m][i][r], x[i].top - top);
+      x[i].top = top;
 #pragma unroll
-          for (int j = 2 * b; j < 2 * b + 2; ++j) f[i][j] *= (half8v){h, h, h, h, h, h, h, h};
-        }
+      for (int b = 0; b < 4; ++b) {
+        const _Float16 h = __builtin_amdgcn_ldexph((_Float16)1.0f, e[b] - top);  // 0 below 2^-24
+#pragma unroll
+        for (int j = 2 * b; j < 2 * b + 2; ++j) f[i][j] *= (half8v){h, h, h, h, h, h, h, h};
       }
     }
+  }
+};
+
+template <int NM, int NT, bool POWERS>
+__device__ __forceinline__ void multiply(const Codes (&c)[NM], const Columns<NT, POWERS> &x, float4v (&acc)[NM][NT]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      const half8v w = weights(c[m], j);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x.f[i][j], acc[m][i], 0, 0, 0);
+    }
+}
+
+// A wave's 16-row tiles of NM matrices, a step of codes at a time (q and s: matrix
+// m's codes and scales, from its tile's first row on).
+//  ALIGNED: fetch() starts a step's way into LDS (ring: NM kTile bytes of the wave's
+//  own), take() reads it back once it has landed: a transfer takes eight rows' whole
+//  128 bytes, where loads in the matrix instruction's order touch 16 rows with every
+//  16 lanes, 64 line lookups for the 1 KB that 8 lines hold (15% of the layer).
+//  Otherwise fetch() loads straight into registers, at any alignment.
+constexpr uint32_t kTile = 16 * 128 + 16 * 16;  // codes, then scales
+template <int NM, bool ALIGNED>
+struct Tiles {
+  const uint8_t *q[NM], *s[NM];
+  uint8_t *ring;
+  uint32_t K;
+  Codes next[ALIGNED ? 1 : NM];
+
+  __device__ __forceinline__ void fetch(uint32_t k0) {
+    const uint32_t lane = threadIdx.x % 64;
+    if constexpr (ALIGNED) {
+      const uint32_t row = lane / 8, sw = swz128(row);  // (row + 8 has the phase sw ^ 4)
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
-        const half8v w = weights(c[m], j);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, f[i][j], acc[m][i], 0, 0, 0);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t piece = lane % 8 ^ (sw ^ (h ? 4u : 0u));
+          if (k0 + piece * 32 < K)
+            __builtin_amdgcn_global_load_lds((glb_void *)(q[m] + (uint64_t)(row + 8 * h) * (K / 2) + k0 / 2 + piece * 16),
+                                             (lds_void *)(ring + m * kTile + h * 1024), 16, 0, 0);
+        }
+        if (k0 + lane % 4 * 64 < K)
+          __builtin_amdgcn_global_load_lds((glb_void *)(s[m] + (uint64_t)(lane / 4) * (K / 16) + k0 / 16 + lane % 4 * 4),
+                                           (lds_void *)(ring + m * kTile + 2048), 4, 0, 0);
       }
+    } else {
+      const uint32_t l16 = lane % 16, k = k0 + lane / 16 * 64;
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+        next[m] = load_codes(q[m] + (uint64_t)l16 * (K / 2), s[m] + (uint64_t)l16 * (K / 16), k, K, k0 + CH <= K);
+    }
+  }
+  // after a wait for the step's loads; ends when LDS has been read
+  __device__ __forceinline__ void take(uint32_t k0, Codes (&c)[NM]) {
+    const uint32_t lane = threadIdx.x % 64, l16 = lane % 16, lq = lane / 16;
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      if constexpr (ALIGNED) {
+        const uint8_t *at = ring + m * kTile;
+        c[m].lo = *reinterpret_cast<const u32x4 *>(at + l16 * 128 + (2 * lq ^ swz128(l16)) * 16);
+        c[m].hi = *reinterpret_cast<const u32x4 *>(at + l16 * 128 + ((2 * lq + 1) ^ swz128(l16)) * 16);
+        // past K the columns are finite, and so is any code; a scale need not be
+        c[m].s = k0 + lq * 64 < K ? *reinterpret_cast<const uint32_t *>(at + 2048 + l16 * 16 + lq * 4) : 0u;
+      } else {
+        c[m] = next[m];
+      }
+    }
+    wait_lgkm0();
+    asm volatile("" ::: "memory");
+  }
+};
+
+// acc[m] += 16 rows of matrix m x one tile of 16 columns, over the steps k0 = first,
+// first + turn, ... of 256 each; the columns straight from memory.
+template <int NM, bool ALIGNED, bool POWERS>
+__device__ __forceinline__ void products(Tiles<NM, ALIGNED> &w, ColumnData (&x)[1], uint32_t first, uint32_t turn,
+                                         float4v (&acc)[NM][1]) {
+  const uint32_t lq = (threadIdx.x % 64) / 16, K = w.K;
+  if (ALIGNED && first < K) w.fetch(first);
+  for (uint32_t k0 = first; k0 < K; k0 += turn) {
+    if constexpr (!ALIGNED) w.fetch(k0);
+    Columns<1, POWERS> col;
+    col.load(x, k0 + lq * 64, K);
+    if constexpr (ALIGNED) {
+      wait_vm<0>();  // this step's codes (and columns)
+      asm volatile("" ::: "memory");
+    }
+    Codes c[NM];
+    w.take(k0, c);
+    if (ALIGNED && k0 + turn < K) w.fetch(k0 + turn);  // behind this step's products
+    if constexpr (POWERS) col.align(x, k0 + lq * 64, K, acc);
+    multiply(c, col, acc);
+  }
+}
+
+// The same for NT tiles of columns and all four waves in step: the workgroup brings
+// a step of its columns (512 bytes each) into LDS once, two columns a transfer, two
+// buffers at cols (NT 16 KB), and every wave reads the fragments there, conflict free:
+// piece p of column c is stored at p ^ (c % 16).  row(c): column c's values, or null
+// where there is none (what LDS holds there reaches only its own column of the
+// result).
+template <int NM, int NT, bool ALIGNED, bool POWERS, typename Row>
+__device__ __forceinline__ void products_many(Tiles<NM, ALIGNED> &w, ColumnData (&x)[NT], Row row, uint8_t *cols,
+                                              float4v (&acc)[NM][NT]) {
+  const uint32_t lane = threadIdx.x % 64, l16 = lane % 16, lq = lane / 16, K = w.K;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const _Float16 *from[NT * 2];
+#pragma unroll
+  for (int i = 0; i < NT * 2; ++i) from[i] = row((i * 4 + wave) * 2 + lane / 32);
+  auto bring = [&](uint32_t buf, uint32_t k0) {
+#pragma unroll
+    for (int i = 0; i < NT * 2; ++i) {
+      const uint32_t t = i * 4 + wave, c = t * 2 + lane / 32;
+      const uint32_t piece = lane % 32 ^ c % 16;
+      // a piece past K would meet zero weights: the column's first one stands in
+      const uint32_t k = k0 + piece * 8 < K ? k0 + piece * 8 : 0u;
+      if (from[i])
+        __builtin_amdgcn_global_load_lds((glb_void *)(from[i] + k), (lds_void *)(cols + buf * NT * 8192 + t * 1024), 16, 0,
+                                         0);
+    }
+  };
+  uint32_t buf = 0;
+  bring(0, 0);
+  w.fetch(0);
+  for (uint32_t k0 = 0; k0 < K; k0 += CH) {
+    const uint32_t k = k0 + lq * 64;
+    wait_vm<0>();  // this wave's part of the step
+    asm volatile("" ::: "memory");
+    Codes c[NM];
+    w.take(k0, c);  // (and the wave's reads of the other buffer are done)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (k0 + CH < K) {
+      bring(buf ^ 1, k0 + CH);
+      w.fetch(k0 + CH);
+    }
+    Columns<NT, POWERS> col;
+    const uint8_t *st = cols + buf * NT * 8192;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        col.f[i][j] = *reinterpret_cast<const half8v *>(st + (i * 16 + l16) * 512 + ((lq * 8 + j) ^ l16) * 16);
+      if constexpr (POWERS) col.load_powers(x[i], i, k, K);
+    }
+    if constexpr (POWERS) col.align(x, k, K, acc);
+    multiply(c, col, acc);
+    buf ^= 1;
   }
 }
 
@@ -398,66 +531,91 @@ struct Column {
 
 constexpr uint32_t kOwnSlots = 16;  // slots up to which one kernel does down and combine
 
-// PX planes of x, PH planes of h, NT tiles of 16 columns a pass, RT tiles of 16 rows
-// of h a workgroup
-template <int PX, int PH, int NT, int RT, bool ALIGNED>
+// Which expert a workgroup works for, and its tokens.
+struct Work {
+  int32_t e;
+  uint32_t total;  // 0: none
+  __device__ __forceinline__ Work(const MoeDecodeParams &p, uint32_t item, uint32_t N, uint32_t *list) {
+    e = __builtin_amdgcn_readfirstlane(p.S <= p.E ? p.ids[item] : (int32_t)item);
+    uint32_t first;
+    total = find_tokens(p.ids, p.S, e, 0, N, list, &first);
+    if (p.S <= p.E && first != item) total = 0;  // the same in every wave
+  }
+};
+
+// the tiles of gate rows and up rows from r0 on (I % 16 == 0: a tile is whole, or past
+// I, and reads the last one again)
+template <bool ALIGNED>
+__device__ __forceinline__ void gate_up_tiles(const MoeDecodeParams &p, int32_t e, uint32_t r0, uint8_t *ring,
+                                              Tiles<2, ALIGNED> &w) {
+  w.K = p.H;
+  w.ring = ring;
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const uint64_t row = ((uint64_t)e * 2 + m) * p.I + min(r0, p.I - 16);
+    w.q[m] = p.gu_q + row * (p.H / 2);
+    w.s[m] = p.gu_s + row * (p.H / 16);
+  }
+}
+
+template <int RT, bool ALIGNED>
+__device__ __forceinline__ void down_tiles(const MoeDecodeParams &p, int32_t e, uint32_t r0, uint8_t *ring,
+                                           Tiles<RT, ALIGNED> &w) {
+  w.K = p.I;
+  w.ring = ring;
+#pragma unroll
+  for (int m = 0; m < RT; ++m) {
+    const uint64_t row = (uint64_t)e * p.H + min(r0 + m * 16, p.H - 16);
+    w.q[m] = p.d_q + row * (p.I / 2);
+    w.s[m] = p.d_s + row * (p.I / 16);
+  }
+}
+
+// PX planes of x, PH planes of h; 16 rows of h a workgroup, one tile of columns a pass
+template <int PX, int PH, bool ALIGNED>
 __global__ __launch_bounds__(256) void decode_gate_up_kernel(MoeDecodeParams p) {
-  constexpr uint32_t TP = kTokens<PX>, N = NT * TP, NW = 4, NM = 2 * RT;
-  __shared__ __attribute__((aligned(16))) float red[NW][NM][NT * 16][20];  // [wave][gates, ups][column][row]
+  constexpr uint32_t N = kTokens<PX>, NW = 4;
+  // the waves' steps of codes, then their sums [wave][gate, up][column][row]
+  constexpr uint32_t RED = NW * 2 * 16 * 20 * 4, RING = ALIGNED ? NW * 2 * kTile : 0;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RED > RING ? RED : RING];
+  float(*red)[2][16][20] = reinterpret_cast<float(*)[2][16][20]>(smem);
   __shared__ uint32_t lists[NW][N];
   const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64;
   const uint32_t l16 = lane % 16, lq = lane / 16;
-  const uint32_t item = blockIdx.x / p.tiles_i, r0 = (blockIdx.x % p.tiles_i) * (16 * RT);
-  const int32_t e = __builtin_amdgcn_readfirstlane(p.S <= p.E ? p.ids[item] : (int32_t)item);
+  const uint32_t item = blockIdx.x / p.tiles_i, r0 = (blockIdx.x % p.tiles_i) * 16;
   uint32_t *list = lists[wave];
-  uint32_t first;
-  const uint32_t total = find_tokens(p.ids, p.S, e, 0, N, list, &first);
-  if (total == 0 || (p.S <= p.E && first != item)) return;  // the same in every wave
-  const uint32_t K = p.H, I = p.I;
-  const uint8_t *q[NM], *sc[NM];
+  const Work work(p, item, N, list);
+  if (work.total == 0) return;
+  const uint32_t I = p.I;
+  Tiles<2, ALIGNED> w;
+  gate_up_tiles(p, work.e, r0, smem + wave * 2 * kTile, w);
+  const float g = p.gu_g[work.e];
+  for (uint32_t t0 = 0; t0 < work.total; t0 += N) {
+    uint32_t first;
+    if (t0 > 0) find_tokens(p.ids, p.S, work.e, t0, N, list, &first);
+    const uint32_t cnt = min(work.total - t0, N);
+    const Column<PX> c(list, 0, cnt);
+    ColumnData x[1];
+    x[0].row = p.xp + ((int64_t)(l16 / N) * p.T + c.slot / p.k) * p.H;
+    x[0].in = c.in;
+    float4v acc[2][1] = {{{0, 0, 0, 0}}, {{0, 0, 0, 0}}};
+    if (t0 > 0) __syncthreads();  // the last pass's sums have been read: LDS takes codes again
+    products<2, ALIGNED, false>(w, x, wave * CH, NW * CH, acc);
+    __syncthreads();  // every wave is done with its codes
 #pragma unroll
-  for (int m = 0; m < NM; ++m) {
-    // I % 16 == 0: a tile is whole, or past I (and reads the last one again)
-    const uint64_t row = ((uint64_t)e * 2 + m / RT) * I + min(r0 + m % RT * 16, I - 16) + l16;
-    q[m] = p.gu_q + row * (K / 2);
-    sc[m] = p.gu_s + row * (K / 16);
-  }
-  const float g = p.gu_g[e];
-  for (uint32_t t0 = 0; t0 < total; t0 += N) {
-    if (t0 > 0) find_tokens(p.ids, p.S, e, t0, N, list, &first);
-    const uint32_t cnt = min(total - t0, N);
-    ColumnData x[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const Column<PX> c(list, i, cnt);
-      x[i].row = p.xp + ((int64_t)(l16 / TP) * p.T + c.slot / p.k) * K;
-      x[i].in = c.in;
-    }
-    float4v acc[NM][NT];
-#pragma unroll
-    for (int m = 0; m < NM; ++m)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) acc[m][i] = (float4v){0, 0, 0, 0};
-    products<NM, NT, ALIGNED, false>(q, sc, x, K, wave * CH, NW * CH, acc);
-    __syncthreads();  // the last pass's sums have been read
-#pragma unroll
-    for (int m = 0; m < NM; ++m)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) *reinterpret_cast<float4v *>(&red[wave][m][i * 16 + l16][4 * lq]) = acc[m][i];
+    for (int m = 0; m < 2; ++m) *reinterpret_cast<float4v *>(&red[wave][m][l16][4 * lq]) = acc[m][0];
     __syncthreads();
-    for (uint32_t c = tid / (16 * RT); c < cnt; c += 16 / RT) {
-      const uint32_t r = tid % 16, rt = tid / 16 % RT;
-      if (r0 + rt * 16 >= I) continue;
+    const uint32_t tc = tid / 16, r = tid % 16;
+    if (tc < cnt) {
       float zg = 0.0f, zu = 0.0f;
 #pragma unroll
       for (int pl = 0; pl < PX; ++pl)
 #pragma unroll
-        for (uint32_t w = 0; w < NW; ++w) {
-          const uint32_t col = c / TP * 16 + pl * TP + c % TP;
-          zg += red[w][rt][col][r];
-          zu += red[w][RT + rt][col][r];
+        for (uint32_t v = 0; v < NW; ++v) {
+          zg += red[v][0][pl * N + tc][r];
+          zu += red[v][1][pl * N + tc][r];
         }
-      const uint32_t slot = list[c];
+      const uint32_t slot = list[tc];
       const int32_t xe = p.xe[slot / p.k];
       const float h = silu(__builtin_ldexpf(zg * g, xe)) * __builtin_ldexpf(zu * g, xe);
       // the 16 rows are a row of 16 lanes: their power is one exchange away
@@ -470,8 +628,8 @@ __global__ __launch_bounds__(256) void decode_gate_up_kernel(MoeDecodeParams p) 
       _Float16 o[PH];
       split<PH>(__builtin_ldexpf(h, -he), o);
 #pragma unroll
-      for (int pl = 0; pl < PH; ++pl) p.h[((int64_t)pl * p.S + slot) * I + r0 + rt * 16 + r] = o[pl];
-      if (r == 0) p.he[(int64_t)slot * p.he_ld + r0 / 16 + rt] = (int8_t)he;
+      for (int pl = 0; pl < PH; ++pl) p.h[((int64_t)pl * p.S + slot) * I + r0 + r] = o[pl];
+      if (r == 0) p.he[(int64_t)slot * p.he_ld + r0 / 16] = (int8_t)he;
     }
   }
 }
@@ -488,40 +646,150 @@ __device__ __forceinline__ float4v join_planes(float4v v) {
   return o;
 }
 
-// y[slot][H] = w (Wd h), 64 RT rows of one expert: a wave per 16 RT
-template <int PH, int NT, int RT, bool ALIGNED>
-__global__ __launch_bounds__(256) void decode_down_kernel(MoeDecodeParams p) {
-  constexpr uint32_t TP = kTokens<PH>, N = NT * TP, NW = 4;
+// Many tokens an expert: 64 rows of h a workgroup, 16 a wave, NT tiles of columns a
+// pass, which the waves share.
+template <int PX, int PH, int NT, bool ALIGNED>
+__global__ __launch_bounds__(256) void decode_gate_up_many_kernel(MoeDecodeParams p) {
+  constexpr uint32_t TP = kTokens<PX>, N = NT * TP, NW = 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t cols[NT * 16384];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[ALIGNED ? NW * 2 * kTile : 16];
   __shared__ uint32_t lists[NW][N];
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+  const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64;
   const uint32_t l16 = lane % 16, lq = lane / 16;
-  const uint32_t item = blockIdx.x / p.tiles_h, r0 = (blockIdx.x % p.tiles_h) * (64 * RT) + wave * (16 * RT);
-  const uint32_t K = p.I, H = p.H;
-  if (r0 >= H) return;  // no barriers below
-  const int32_t e = __builtin_amdgcn_readfirstlane(p.S <= p.E ? p.ids[item] : (int32_t)item);
+  const uint32_t item = blockIdx.x / p.tiles_i, r0 = (blockIdx.x % p.tiles_i) * 64 + wave * 16;
   uint32_t *list = lists[wave];
-  uint32_t first;
-  const uint32_t total = find_tokens(p.ids, p.S, e, 0, N, list, &first);
-  if (total == 0 || (p.S <= p.E && first != item)) return;
-  const uint8_t *q[RT], *sc[RT];
+  const Work work(p, item, N, list);
+  if (work.total == 0) return;
+  Tiles<2, ALIGNED> w;
+  gate_up_tiles(p, work.e, r0, ring + (ALIGNED ? wave * 2 * kTile : 0), w);
+  const float g = p.gu_g[work.e];
+  for (uint32_t t0 = 0; t0 < work.total; t0 += N) {
+    uint32_t first;
+    if (t0 > 0) {
+      find_tokens(p.ids, p.S, work.e, t0, N, list, &first);
+      __syncthreads();  // every wave is done with the last pass's columns
+    }
+    const uint32_t cnt = min(work.total - t0, N);
+    ColumnData x[NT];
+    float4v acc[2][NT];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[m][i] = (float4v){0, 0, 0, 0};
+    products_many<2, NT, ALIGNED, false>(
+        w, x,
+        [&](uint32_t c) -> const _Float16 * {
+          const uint32_t t = c / 16 * TP + c % TP;
+          return t < cnt ? p.xp + ((int64_t)(c % 16 / TP) * p.T + list[t] / p.k) * p.H : nullptr;
+        },
+        cols, acc);
+    if (r0 >= p.I) continue;  // (after the pass's barriers)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const float4v zg = join_planes<PX>(acc[0][i]), zu = join_planes<PX>(acc[1][i]);
+      const Column<PX> c(list, i, cnt);
+      const int32_t xe = c.in ? p.xe[c.slot / p.k] : 0;
+      float h[4], top = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        h[r] = silu(__builtin_ldexpf(zg[r] * g, xe)) * __builtin_ldexpf(zu[r] * g, xe);
+        top = fmaxf(top, fabsf(h[r]));
+      }
+      // a column's 16 rows are in its four lane quarters
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const int32_t he = power_of(top);
+      if (l16 < TP && c.in) {  // plane 0 holds the sums
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          _Float16 o[PH];
+          split<PH>(__builtin_ldexpf(h[r], -he), o);
+#pragma unroll
+          for (int pl = 0; pl < PH; ++pl) p.h[((int64_t)pl * p.S + c.slot) * p.I + r0 + 4 * lq + r] = o[pl];
+        }
+        if (lq == 0) p.he[(int64_t)c.slot * p.he_ld + r0 / 16] = (int8_t)he;
+      }
+    }
+  }
+}
+
+// the sums of a column tile, times the routing weight, to y
+template <int PH, int RT, int NT>
+__device__ __forceinline__ void store_y(const MoeDecodeParams &p, const float4v (&acc)[RT][NT], int i, uint32_t slot,
+                                        const ColumnData &h, float g, uint32_t r0) {
+  const uint32_t lane = threadIdx.x % 64, l16 = lane % 16, lq = lane / 16;
+  const float f = h.in ? g * p.w[slot] : 0.0f;
 #pragma unroll
   for (int m = 0; m < RT; ++m) {
-    // H % 16 == 0: a tile is whole, or past H (and reads the last one again)
-    const uint64_t row = (uint64_t)e * H + min(r0 + m * 16, H - 16) + l16;
-    q[m] = p.d_q + row * (K / 2);
-    sc[m] = p.d_s + row * (K / 16);
+    float4v v = join_planes<PH>(acc[m][i]);
+    if (l16 < kTokens<PH> && h.in && r0 + m * 16 < p.H) {  // plane 0
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = __builtin_ldexpf(v[r] * f, h.top);
+      *reinterpret_cast<float4v *>(p.y + (int64_t)slot * p.H + r0 + m * 16 + 4 * lq) = v;
+    }
   }
-  const float g = p.d_g[e];
-  for (uint32_t t0 = 0; t0 < total; t0 += N) {
-    if (t0 > 0) find_tokens(p.ids, p.S, e, t0, N, list, &first);
-    const uint32_t cnt = min(total - t0, N);
+}
+
+// y[slot][H] = w (Wd h), 64 RT rows of one expert: a wave per 16 RT, one tile of
+// columns a pass
+template <int PH, int RT, bool ALIGNED>
+__global__ __launch_bounds__(256) void decode_down_kernel(MoeDecodeParams p) {
+  constexpr uint32_t N = kTokens<PH>, NW = 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[ALIGNED ? NW * RT * kTile : 16];
+  __shared__ uint32_t lists[NW][N];
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l16 = threadIdx.x % 16;
+  const uint32_t item = blockIdx.x / p.tiles_h, r0 = (blockIdx.x % p.tiles_h) * (64 * RT) + wave * (16 * RT);
+  if (r0 >= p.H) return;  // no barriers below
+  uint32_t *list = lists[wave];
+  const Work work(p, item, N, list);
+  if (work.total == 0) return;
+  Tiles<RT, ALIGNED> w;
+  down_tiles<RT>(p, work.e, r0, ring + (ALIGNED ? wave * RT * kTile : 0), w);
+  const float g = p.d_g[work.e];
+  for (uint32_t t0 = 0; t0 < work.total; t0 += N) {
+    uint32_t first;
+    if (t0 > 0) find_tokens(p.ids, p.S, work.e, t0, N, list, &first);
+    const Column<PH> c(list, 0, min(work.total - t0, N));
+    ColumnData h[1];
+    h[0].row = p.h + ((int64_t)(l16 / N) * p.S + c.slot) * p.I;
+    h[0].powers = p.he + (int64_t)c.slot * p.he_ld;
+    h[0].in = c.in;
+    h[0].top = kNoPower;
+    float4v acc[RT][1];
+#pragma unroll
+    for (int m = 0; m < RT; ++m) acc[m][0] = (float4v){0, 0, 0, 0};
+    products<RT, ALIGNED, true>(w, h, 0, CH, acc);
+    store_y<PH>(p, acc, 0, c.slot, h[0], g, r0);
+  }
+}
+
+template <int PH, int NT, int RT, bool ALIGNED>
+__global__ __launch_bounds__(256) void decode_down_many_kernel(MoeDecodeParams p) {
+  constexpr uint32_t TP = kTokens<PH>, N = NT * TP, NW = 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t cols[NT * 16384];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[ALIGNED ? NW * RT * kTile : 16];
+  __shared__ uint32_t lists[NW][N];
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t item = blockIdx.x / p.tiles_h, r0 = (blockIdx.x % p.tiles_h) * (64 * RT) + wave * (16 * RT);
+  uint32_t *list = lists[wave];
+  const Work work(p, item, N, list);
+  if (work.total == 0) return;
+  Tiles<RT, ALIGNED> w;
+  down_tiles<RT>(p, work.e, r0, ring + (ALIGNED ? wave * RT * kTile : 0), w);
+  const float g = p.d_g[work.e];
+  for (uint32_t t0 = 0; t0 < work.total; t0 += N) {
+    uint32_t first;
+    if (t0 > 0) {
+      find_tokens(p.ids, p.S, work.e, t0, N, list, &first);
+      __syncthreads();  // every wave is done with the last pass's columns
+    }
+    const uint32_t cnt = min(work.total - t0, N);
     ColumnData h[NT];
     uint32_t slot[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const Column<PH> c(list, i, cnt);
       slot[i] = c.slot;
-      h[i].row = p.h + ((int64_t)(l16 / TP) * p.S + c.slot) * K;
       h[i].powers = p.he + (int64_t)c.slot * p.he_ld;
       h[i].in = c.in;
       h[i].top = kNoPower;
@@ -531,20 +799,15 @@ __global__ __launch_bounds__(256) void decode_down_kernel(MoeDecodeParams p) {
     for (int m = 0; m < RT; ++m)
 #pragma unroll
       for (int i = 0; i < NT; ++i) acc[m][i] = (float4v){0, 0, 0, 0};
-    products<RT, NT, ALIGNED, true>(q, sc, h, K, 0, CH, acc);
+    products_many<RT, NT, ALIGNED, true>(
+        w, h,
+        [&](uint32_t c) -> const _Float16 * {
+          const uint32_t t = c / 16 * TP + c % TP;
+          return t < cnt ? p.h + ((int64_t)(c % 16 / TP) * p.S + list[t]) * p.I : nullptr;
+        },
+        cols, acc);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const float f = h[i].in ? g * p.w[slot[i]] : 0.0f;
-#pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        float4v v = join_planes<PH>(acc[m][i]);
-        if (l16 < TP && h[i].in && r0 + m * 16 < H) {  // plane 0
-#pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = __builtin_ldexpf(v[r] * f, h[i].top);
-          *reinterpret_cast<float4v *>(p.y + (int64_t)slot[i] * H + r0 + m * 16 + 4 * lq) = v;
-        }
-      }
-    }
+    for (int i = 0; i < NT; ++i) store_y<PH>(p, acc, i, slot[i], h[i], g, r0);
   }
 }
 
@@ -576,9 +839,10 @@ template <int PH, bool ALIGNED, typename OutT>
 __global__ __launch_bounds__(1024) void decode_own_kernel(MoeDecodeParams p) {
   constexpr uint32_t NW = 16, TP = kTokens<PH>;
   __shared__ __attribute__((aligned(16))) float sum[NW][kOwnSlots][16];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[ALIGNED ? NW * kTile : 16];
   const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64;
   const uint32_t l16 = lane % 16, lq = lane / 16;
-  const uint32_t r0 = blockIdx.x * 16, K = p.I, H = p.H;
+  const uint32_t r0 = blockIdx.x * 16, K = p.I;
   if (tid < p.T * 16)
 #pragma unroll
     for (uint32_t w = 0; w < NW; ++w) sum[w][tid / 16][tid % 16] = 0.0f;
@@ -589,17 +853,16 @@ __global__ __launch_bounds__(1024) void decode_own_kernel(MoeDecodeParams p) {
   for (uint32_t unit = wave; unit < p.S * parts; unit += NW) {
     const uint32_t slot = unit / parts, part = unit % parts;
     const int32_t e = p.ids[slot];
-    const uint64_t row = (uint64_t)e * H + r0 + l16;
-    const uint8_t *dq = p.d_q + row * (K / 2), *ds = p.d_s + row * (K / 16);
+    Tiles<1, ALIGNED> w;
+    down_tiles<1>(p, e, r0, ring + (ALIGNED ? wave * kTile : 0), w);
     const float fac = p.d_g[e] * p.w[slot];
     ColumnData h[1];
     h[0].in = l16 % TP == 0;  // a column for each plane
     h[0].row = p.h + ((int64_t)(l16 / TP) * p.S + slot) * K;
     h[0].powers = p.he + (int64_t)slot * p.he_ld;
     h[0].top = kNoPower;
-    const uint8_t *const q[1] = {dq}, *const sc[1] = {ds};
     float4v a[1][1] = {{{0, 0, 0, 0}}};
-    products<1, 1, ALIGNED, true>(q, sc, h, K, part * CH, parts * CH, a);
+    products<1, ALIGNED, true>(w, h, part * CH, parts * CH, a);
     const float4v acc = join_planes<PH>(a[0][0]);
     if (l16 == 0) {
       float4v *at = reinterpret_cast<float4v *>(&sum[wave][slot / p.k][4 * lq]);
@@ -621,31 +884,23 @@ __global__ __launch_bounds__(1024) void decode_own_kernel(MoeDecodeParams p) {
   }
 }
 
-// column tiles a pass, from the tokens an expert has on average: one more pass
-// reads the weights again (from L2), one tile too many costs registers
+// Column tiles a pass, from the tokens an expert has on average: 1 (the columns
+// straight from memory), or 2 or 4 (through LDS, shared).  One more pass reads the
+// weights again, one tile too many costs registers and LDS.
 template <int P>
 int column_tiles(const MoeDecodeParams &p) {
   const uint32_t mean = p.S / min(p.S, p.E);
   return mean * 2 <= kTokens<P> ? 1 : mean <= kTokens<P> ? 2 : 4;
 }
 
-// Row tiles: two (gate_up) and four (down) a wave keep twice and four times the
-// bytes in flight and read the columns as much less often; one while there are few
-// workgroups.
-template <int PX, int PH, int RT, bool ALIGNED>
-void launch_gate_up_rt(MoeDecodeParams p, hipStream_t stream) {
-  p.tiles_i = (p.I + 16 * RT - 1) / (16 * RT);
-  const uint32_t grid = p.tiles_i * min(p.S, p.E);
-  const int nt = column_tiles<PX>(p);
-  if (nt == 1) decode_gate_up_kernel<PX, PH, 1, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
-  else if (nt == 2) decode_gate_up_kernel<PX, PH, 2, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
-  else decode_gate_up_kernel<PX, PH, 4, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
-}
-
 template <int PX, int PH, bool ALIGNED>
-void launch_gate_up(const MoeDecodeParams &p, hipStream_t stream) {
-  if ((uint64_t)(p.I / 16) * min(p.S, p.E) >= RTG_MIN * device_cu_count()) launch_gate_up_rt<PX, PH, 2, ALIGNED>(p, stream);
-  else launch_gate_up_rt<PX, PH, 1, ALIGNED>(p, stream);
+void launch_gate_up(MoeDecodeParams p, hipStream_t stream) {
+  const int nt = column_tiles<PX>(p);
+  p.tiles_i = nt == 1 ? p.I / 16 : (p.I + 63) / 64;
+  const uint32_t grid = p.tiles_i * min(p.S, p.E);
+  if (nt == 1) decode_gate_up_kernel<PX, PH, ALIGNED><<<grid, 256, 0, stream>>>(p);
+  else if (nt == 2) decode_gate_up_many_kernel<PX, PH, 2, ALIGNED><<<grid, 256, 0, stream>>>(p);
+  else decode_gate_up_many_kernel<PX, PH, 4, ALIGNED><<<grid, 256, 0, stream>>>(p);
 }
 
 template <int PH, int RT, bool ALIGNED>
@@ -653,9 +908,9 @@ void launch_down_rt(MoeDecodeParams p, hipStream_t stream) {
   p.tiles_h = (p.H + 64 * RT - 1) / (64 * RT);
   const uint32_t grid = p.tiles_h * min(p.S, p.E);
   const int nt = column_tiles<PH>(p);
-  if (nt == 1) decode_down_kernel<PH, 1, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
-  else if (nt == 2) decode_down_kernel<PH, 2, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
-  else decode_down_kernel<PH, 4, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
+  if (nt == 1) decode_down_kernel<PH, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
+  else if (nt == 2) decode_down_many_kernel<PH, 2, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
+  else decode_down_many_kernel<PH, 4, RT, ALIGNED><<<grid, 256, 0, stream>>>(p);
 }
 
 template <int PH, bool ALIGNED, typename OutT>
@@ -664,7 +919,9 @@ hipError_t launch_down(const MoeDecodeParams &p, hipStream_t stream) {
     decode_own_kernel<PH, ALIGNED, OutT><<<p.H / 16, 1024, 0, stream>>>(p);
     return hipGetLastError();
   }
-  if ((uint64_t)(p.H / 64) * min(p.S, p.E) >= RTD_MIN * device_cu_count()) launch_down_rt<PH, 4, ALIGNED>(p, stream);
+  // two row tiles a wave keep twice the bytes in flight and read the columns half as
+  // often; one while there are few workgroups
+  if ((uint64_t)(p.H / 64) * min(p.S, p.E) >= 8 * device_cu_count()) launch_down_rt<PH, 2, ALIGNED>(p, stream);
   else launch_down_rt<PH, 1, ALIGNED>(p, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
