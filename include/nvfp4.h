@@ -254,7 +254,9 @@ nvfp4_status nvfp4_fp8_gemm(const uint8_t *a_q, const float *a_g,
  *         x_hat = e4m3(q) * s; blocks at the edges are shorter.
  *   s = max(fl(amax/448), 2^-126), amax = max|x| of the block; 1 if amax == 0
  *   q = the code nearest the exact quotient x/s (ties to even, sign of x kept).
- * cols > 0, cols % 16 == 0, rows >= 0, rows * cols / 16 < 2^31.  No workspace.
+ * cols > 0, cols % 16 == 0, rows >= 0, rows * cols / 16 < 2^31, fewer than 2^29
+ * scales (2^24 with block_rows 128).  No workspace.  A NaN takes the NaN code and
+ * no part in amax; an infinity makes its block's scale infinite (its values NaN).
  * Alignment of x as for nvfp4_quantize (other layouts take a slower path).
  * ---------------------------------------------------------------------- */
 nvfp4_status nvfp4_fp8_block_quantize(const void *x, nvfp4_dtype x_type,
@@ -269,12 +271,14 @@ nvfp4_status nvfp4_fp8_block_quantize(const void *x, nvfp4_dtype x_type,
  *                   * sum_{k = 128b .. 128b+127, k < K} e4m3(A[m][k]) e4m3(B[n][k])
  * A [M x K] activations with scales [M][ceil(K/128)], B [N x K] weights (one
  * row per output feature) with scales [ceil(N/128)][ceil(K/128)], dense
- * row-major E4M3FN bytes, 16-byte aligned; scales finite.  The blocks are
+ * row-major E4M3FN bytes, 16-byte aligned; scales and products of two of them
+ * finite (what a row of A holds reaches only that row of C).  The blocks are
  * joined in float32 and the result is rounded to c_type.  c_type NVFP4_F32:
  * products exact, float32 sums.  NVFP4_BF16: products through the FP8 matrix
  * unit, which cuts each of eight neighbouring products below 2^-13 of the
- * largest (1.4e-5 of a random result, against the result's own 2^-9).  M, N >= 0; K > 0, K % 16 == 0; c is
- * [M][ldc] of c_type, ldc >= N, aligned to its element.
+ * largest (1.4e-5 of a random result, against the result's own 2^-9).
+ * 0 <= M, N < 2^26, M N < 2^38; K > 0, K % 16 == 0; c is [M][ldc] of c_type,
+ * ldc >= N, aligned to its element.
  * ---------------------------------------------------------------------- */
 nvfp4_status nvfp4_fp8_block_gemm(const uint8_t *a_q, const float *a_s,
                                   const uint8_t *b_q, const float *b_s,
@@ -398,7 +402,9 @@ nvfp4_status nvfp4_moe_combine(const void *y, nvfp4_dtype y_type,
  *         the gate, [I, 2I) the up projection.
  * d_q/d_s/d_g     [E][H][I/2], [E][H][I/16], [E].
  * out     [T][ld_out] of out_type, ld_out >= H; must not overlap x.
- * 1 <= k <= E <= 1024, k <= 32; H, I > 0, multiples of 16, <= 2^20.
+ * 1 <= k <= E <= 1024, k <= 32; H, I > 0, multiples of 16, <= 2^20; E H and
+ * E I < 2^28.  A token's infinities and NaNs (in x or its logits, a row of
+ * -infinity included) reach only its own row of out.
  * T >= 0; more than 128 tokens return NVFP4_ERR_UNSUPPORTED.
  * Any alignment of x, out (their element's), q and s; the fastest path needs
  * H % 64 == 0, I % 64 == 0, 16-byte aligned q and 4-byte aligned s.

@@ -92,10 +92,11 @@ nvfp4_status quantize_impl(const void *x, nvfp4_dtype x_type, int64_t rows, int6
   return from_hip(launch_quantize(p, x_type == NVFP4_BF16, vec, 1, rs, stream));
 }
 
-// shape rules of the few-token routed-expert layer (apart from its token limit)
+// shape rules of the few-token routed-expert layer (apart from its token limit); the
+// last two keep a launch's threads (16 rows of one expert per workgroup) under 2^32
 bool decode_shape_ok(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I) {
   return T >= 0 && E >= 1 && E <= 1024 && k >= 1 && k <= 32 && k <= E && H > 0 && H % 16 == 0 && I > 0 &&
-         I % 16 == 0 && H <= (1 << 20) && I <= (1 << 20);
+         I % 16 == 0 && H <= (1 << 20) && I <= (1 << 20) && H * E < (1 << 28) && I * E < (1 << 28);
 }
 
 // ---------------------------------------------- allocation-free quantize
@@ -323,6 +324,9 @@ nvfp4_status nvfp4_fp8_block_quantize(const void *x, nvfp4_dtype x_type, int64_t
                                       hipStream_t stream) {
   if (!valid_dtype(x_type) || !quant_shape_ok(rows, cols) || ld_x < cols) return NVFP4_ERR_INVALID_ARG;
   if (block_rows != 1 && block_rows != 128) return NVFP4_ERR_INVALID_ARG;
+  // a launch's threads (4 per block of a row, 256 per tile) stay under 2^32
+  const int64_t kb = (cols + 127) / 128, blocks = (rows + block_rows - 1) / block_rows * kb;
+  if (blocks >= (block_rows == 1 ? 1ll << 29 : 1ll << 24)) return NVFP4_ERR_INVALID_ARG;
   if (rows == 0) return NVFP4_OK;
   if (!x || !q || !s || !aligned16(q) || ((uintptr_t)s & 3u)) return NVFP4_ERR_INVALID_ARG;
   if (((uintptr_t)x % dtype_size(x_type)) || ld_x > kI32Max * 64ll) return NVFP4_ERR_INVALID_ARG;
@@ -334,9 +338,8 @@ nvfp4_status nvfp4_fp8_block_quantize(const void *x, nvfp4_dtype x_type, int64_t
   p.rows = (uint32_t)rows;
   p.cols = (uint32_t)cols;
   p.block_rows = (uint32_t)block_rows;
-  const uint32_t kb = (uint32_t)((cols + 127) / 128);
-  p.blocks = (uint32_t)((rows + block_rows - 1) / block_rows) * kb;
-  p.div_kb = FastDiv(kb);
+  p.blocks = (uint32_t)blocks;
+  p.div_kb = FastDiv((uint32_t)kb);
   p.q = q;
   p.s = s;
   const bool vec = aligned16(x) && (ld_x * (int64_t)dtype_size(x_type)) % 16 == 0;
@@ -348,7 +351,8 @@ nvfp4_status nvfp4_fp8_block_gemm(const uint8_t *a_q, const float *a_s, const ui
                                   nvfp4_dtype c_type, int64_t ldc, hipStream_t stream) {
   if (!valid_dtype(c_type) || M < 0 || N < 0 || K <= 0 || K % 16 != 0 || ldc < N)
     return NVFP4_ERR_INVALID_ARG;
-  if (M > kI32Max || N > kI32Max || K > kI32Max) return NVFP4_ERR_INVALID_ARG;
+  // a launch's threads (one row of 16 x 16 tiles has 64 per column) stay under 2^32
+  if (M >= (1 << 26) || N >= (1 << 26) || M * N >= (1ll << 38) || K > kI32Max) return NVFP4_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return NVFP4_OK;
   if (!a_q || !a_s || !b_q || !b_s || !c || !aligned16(a_q) || !aligned16(b_q) || ((uintptr_t)a_s & 3u) ||
       ((uintptr_t)b_s & 3u) || (uintptr_t)c % dtype_size(c_type))

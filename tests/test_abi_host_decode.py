@@ -114,3 +114,16 @@ def test_binding_refuses_cpu_tensors_and_bad_shapes(lib):
             B.nvfp4_moe_decode(*bad)
     with pytest.raises(ValueError, match="out"):
         B.nvfp4_moe_decode(x, lg, 2, gu, dn, out=torch.zeros((T, H + 16)))
+
+
+def test_largest_sizes(lib):
+    """Shapes whose launches would pass 2^32 threads are refused, whatever the card's memory."""
+    q = lib.nvfp4_fp8_block_quantize
+    assert q(FAKE, B.NVFP4_BF16, 2 ** 29, 16, 16, 1, FAKE, FAKE, None) == INVALID
+    assert q(FAKE, B.NVFP4_BF16, 128, 2 ** 31 - 16, 2 ** 31, 128, FAKE, FAKE, None) == INVALID
+    assert q(FAKE, B.NVFP4_BF16, 1, 2 ** 31 - 16, 2 ** 31, 128, FAKE, FAKE, None) == INVALID
+    g = lib.nvfp4_fp8_block_gemm
+    for M, N in ((2 ** 26, 1), (1, 2 ** 26), (2 ** 19, 2 ** 19), (2 ** 26 - 1, 2 ** 26 - 1)):
+        assert g(FAKE, FAKE, FAKE, FAKE, M, N, 16, FAKE, B.NVFP4_F32, N, None) == INVALID, (M, N)
+    f = lib.nvfp4_moe_decode_workspace_size
+    assert f(1, 1024, 1, 2 ** 18, 16) == 0 and f(1, 1024, 1, 16, 2 ** 18) == 0 and f(1, 1023, 1, 2 ** 18, 16) > 0
