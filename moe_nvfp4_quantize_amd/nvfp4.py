@@ -153,10 +153,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on_stream(device, stream, body):
+def _on_stream(device, stream, tensors, body):
     """body(raw stream) with ``device`` current and ``stream`` (default: the
     device's current one) as its current stream: what it allocates belongs to
-    the stream that its kernels run on."""
+    the stream that its kernels run on.  ``tensors`` came from elsewhere: a given
+    stream is recorded on them, so that memory freed after the call is not handed
+    out again before the kernels have run."""
     if stream is None and torch.cuda.current_device() == device.index:
         return body(_raw_stream(device.index))
     with torch.cuda.device(device):
@@ -165,7 +167,10 @@ def _on_stream(device, stream, body):
         if stream.device != device:
             raise ValueError("stream and tensors are on different GPUs")
         with torch.cuda.stream(stream):
-            return body(stream.cuda_stream)
+            r = body(stream.cuda_stream)
+        for t in tensors:
+            t.record_stream(stream)
+        return r
 
 
 def _rows(t, rows, cols, what):
@@ -427,7 +432,8 @@ def nvfp4_fp8_block_quantize(x, block_rows=1, out=None, stream=None):
     if out is not None:
         _dense(out[0], torch.uint8, (rows, cols), "q")
         _dense(out[1], torch.float32, s_shape, "s")
-    dev = _one_device(x, *(out or ()))
+    tensors = (x, *(out or ()))
+    dev = _one_device(*tensors)
 
     def body(hs):
         q, s = out if out is not None else (torch.empty((rows, cols), dtype=torch.uint8, device=dev),
@@ -437,7 +443,7 @@ def nvfp4_fp8_block_quantize(x, block_rows=1, out=None, stream=None):
         _check("nvfp4_fp8_block_quantize", st)
         return q, s
 
-    return _on_stream(dev, stream, body)
+    return _on_stream(dev, stream, tensors, body)
 
 
 def nvfp4_fp8_block_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
@@ -458,7 +464,8 @@ def nvfp4_fp8_block_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
     _dense(b_s, torch.float32, (ceil_div(N, 128), kb), "b's s")
     ldc = N if out is None else _rows(out, M, N, "out")
     code = _dtype_code(out_dtype if out is None else out.dtype)
-    dev = _one_device(a_q, a_s, b_q, b_s, *(() if out is None else (out,)))
+    tensors = (a_q, a_s, b_q, b_s) if out is None else (a_q, a_s, b_q, b_s, out)
+    dev = _one_device(*tensors)
 
     def body(hs):
         c = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
@@ -467,7 +474,7 @@ def nvfp4_fp8_block_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
         _check("nvfp4_fp8_block_gemm", st)
         return c
 
-    return _on_stream(dev, stream, body)
+    return _on_stream(dev, stream, tensors, body)
 
 
 # ----------------------------------------------------------------------- MoE
@@ -598,7 +605,8 @@ def nvfp4_moe_decode(x, logits, k, w_gate_up, w_down, out_dtype=torch.bfloat16, 
     _dense(d_s, torch.uint8, (E, H, I // 16), "w_down's s")
     _dense(d_g, torch.float32, (E,), "w_down's g")
     ld_out = H if out is None else _rows(out, T, H, "out")
-    dev = _one_device(x, logits, gu_q, gu_s, gu_g, d_q, d_s, d_g, *(() if out is None else (out,)))
+    tensors = (x, logits, *w_gate_up, *w_down) if out is None else (x, logits, *w_gate_up, *w_down, out)
+    dev = _one_device(*tensors)
     x_code, o_code = _dtype_code(x.dtype), _dtype_code(out_dtype if out is None else out.dtype)
 
     def body(hs):
@@ -610,4 +618,4 @@ def nvfp4_moe_decode(x, logits, k, w_gate_up, w_down, out_dtype=torch.bfloat16, 
         _check("nvfp4_moe_decode", st)
         return o
 
-    return _on_stream(dev, stream, body)
+    return _on_stream(dev, stream, tensors, body)

@@ -222,3 +222,42 @@ def test_quantize_then_gemm_graph_and_stream(B, M):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want), i
+
+
+@pytest.mark.parametrize("M", [3, 40, 140])
+def test_rows_without_numbers_stay_their_own(B, M):
+    """Padding rows of a batch that hold NaN or infinity: NaN rows of C, the others' bits as without."""
+    K, N = 640, 300
+    w = B.nvfp4_fp8_block_quantize(_uneven(N, K, 4, torch.bfloat16), 128)
+    x = _uneven(M, K, 6, torch.bfloat16)
+    for dt in (torch.bfloat16, torch.float32):
+        want = B.nvfp4_fp8_block_gemm(B.nvfp4_fp8_block_quantize(x), w, out_dtype=dt)
+        bad = x.clone()
+        bad[1, 5] = float("nan")
+        bad[M - 1] = float("inf")
+        got = B.nvfp4_fp8_block_gemm(B.nvfp4_fp8_block_quantize(bad), w, out_dtype=dt)
+        assert torch.isnan(got[1]).all() and torch.isnan(got[M - 1]).all()
+        rest = [r for r in range(M) if r not in (1, M - 1)]
+        assert torch.equal(got[rest], want[rest])
+
+
+def test_inputs_freed_behind_a_call_on_another_stream(B):
+    """Memory of inputs dropped after a call on a given stream is not handed out before its
+    kernels have run: the call waits behind other work while the caller frees and fills."""
+    M, K, N = 64, 1280, 390
+    x0 = _uneven(M, K, 6, torch.bfloat16)
+    w = B.nvfp4_fp8_block_quantize(_uneven(N, K, 4, torch.bfloat16), 128)
+    a0 = B.nvfp4_fp8_block_quantize(x0)
+    want = B.nvfp4_fp8_block_gemm(a0, w)
+    side = torch.cuda.Stream()
+    x, a = x0.clone(), tuple(t.clone() for t in a0)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    q, s = B.nvfp4_fp8_block_quantize(x, stream=side)
+    y = B.nvfp4_fp8_block_gemm(a, w, stream=side)
+    del x, a
+    fill = [torch.full_like(t, 1) for t in (x0, *a0)]
+    side.synchronize()
+    assert torch.equal(q, a0[0]) and torch.equal(s, a0[1]) and torch.equal(y, want)
+    assert all(torch.all(t == 1) for t in fill)

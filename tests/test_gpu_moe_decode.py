@@ -180,3 +180,49 @@ def test_decode_step(B):
             tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
         assert np.all(np.abs(got.double().cpu().numpy() - ref) <= tol)
     _check(y, hid, logits, k, gu, dn)
+
+
+@pytest.mark.parametrize("T,E,k", [(3, 8, 2), (24, 40, 3), (100, 6, 2)])
+def test_tokens_without_numbers_stay_their_own(B, T, E, k):
+    """Padding tokens: NaN or infinity in x, a row of logits that a mask left nothing of.  Their own
+    rows are not numbers, the others' bits are as when the padding routes the same way."""
+    x, logits, k, gu, dn = _case(T, E, k, 128, 80, 6)
+    for dt in (torch.bfloat16, torch.float32):
+        want = B.nvfp4_moe_decode(x.to(dt), logits, k, gu, dn, out_dtype=dt)
+        bad, lg = x.to(dt), logits.clone()
+        bad = bad.clone()
+        bad[0, 7] = float("nan")
+        bad[1] = float("inf")
+        lg[2] = float("-inf")
+        got = B.nvfp4_moe_decode(bad, lg, k, gu, dn, out_dtype=dt)
+        assert not torch.isfinite(got[:3]).any()
+        if T > 3:
+            # token 2's experts change where its slots stand, never what others' columns hold
+            err = (got[3:].double() - want[3:].double()).abs().max()
+            assert torch.equal(got[3:], want[3:]), err
+
+
+def test_calls_at_once_on_two_streams(B):
+    """Two layers in flight together, each on a stream of its own, inputs freed behind them."""
+    cases = [_case(20, 16, 3, 256, 128, 4), _case(40, 12, 2, 256, 192, 5)]
+    want = [B.nvfp4_moe_decode(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for st, c in zip(streams * 4, cases * 4):
+        st.wait_stream(torch.cuda.current_stream())
+        x = c[0].clone()
+        st.wait_stream(torch.cuda.current_stream())
+        got.append(B.nvfp4_moe_decode(x, *c[1:], stream=st))
+        del x
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g, want[i % 2]), i
+
+
+def test_one_expert_for_a_whole_batch(B):
+    """Every token of the largest batch on the same experts (several passes over its columns)."""
+    for T, E, k in ((128, 64, 1), (128, 2, 2), (16, 64, 1), (17, 300, 1)):
+        x, logits, k, gu, dn = _case(T, E, k, 192, 80, 9)
+        logits[:] = 0.0
+        logits[:, E - 1] = 5.0
+        _check(B.nvfp4_moe_decode(x, logits, k, gu, dn, out_dtype=torch.float32), x, logits, k, gu, dn)
