@@ -114,7 +114,8 @@ __device__ __forceinline__ Fp8Frag load_frag(const uint8_t *row, uint64_t k, uin
 // workgroup owns 16 columns of 16 rows of C and its NW waves take the 128-column
 // blocks of K in turn, U blocks' loads in flight together, straight into registers
 // (M = 1 reads the same lines of A in every lane group).  The waves' sums are
-// joined through LDS in wave order.
+// joined through LDS in wave order.  Measured: 1 x 5120 x 5120 in 8.8 us (26 MB, 3.0
+// TB/s): launch, three turns of loads and the join, one after the other.
 template <int NW, int U, typename OutT>
 __global__ __launch_bounds__(NW * 64) void block_gemm_rows_kernel(Fp8BlockGemmParams p) {
   __shared__ __attribute__((aligned(16))) float red[NW][16][20];
@@ -176,7 +177,8 @@ __device__ __forceinline__ uint32_t swz128(uint32_t r) { return (r >> 1) & 7u; }
 // before the waves' sums are joined through LDS, in wave order, at the end.  The
 // work is bound by how fast a compute unit takes in its (32 FM + 32 FN) K bytes,
 // which the depth of the stages (not registers) keeps in flight.  The resources
-// end at the matrix's last row: rows past it cost nothing.
+// end at the matrix's last row: rows past it cost nothing.  Measured: 32 x 25600 x
+// 5120 in 30 us (133 MB, 4.4 TB/s); 1000 x 1552 x 2064 float32 in 15 us.
 template <int FM, int FN, int NW, int NST, typename OutT>
 __global__ __launch_bounds__(NW * 64, 1) void block_gemm_strip_kernel(Fp8BlockGemmParams p) {
   using Op = Operand<kExact<OutT>>;
@@ -347,6 +349,10 @@ __global__ __launch_bounds__(NW * 64, 1) void block_gemm_strip_kernel(Fp8BlockGe
 //    16-byte pieces through LDS and stores 16 bytes a lane.
 //  * K % 128 != 0: the last block's pieces past K are zeroed as they are read
 //    (their transfers are pointed at the row's first piece).
+// Measured: 8192 x 25600 x 5120 to bf16 in 1.22 ms (1.76 PFLOP/s; the per-tensor FP8
+// GEMM, which joins nothing, 0.94), bound by the float32 joins beside the matrix
+// instructions (with operands that stay in the cache 1.03); 128 x 151936 x 2048 in
+// 88 us (350 MB, 4.0 TB/s).
 template <int BM, int BN, int NWM, int NWN, int NST, bool VSTORE, typename OutT>
 __global__ __launch_bounds__(NWM *NWN * 64, 1) void block_gemm_tile_kernel(Fp8BlockGemmParams p) {
   constexpr int NW = NWM * NWN, WM = BM / NWM, WN = BN / NWN, FM = WM / 32, FN = WN / 32;

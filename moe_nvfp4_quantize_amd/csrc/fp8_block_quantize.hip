@@ -98,7 +98,8 @@ __device__ __forceinline__ u32x4 encode16(const float v[16], float s) {
 }
 
 // One scale per row and 128 columns: eight lanes per block, U blocks per lane
-// (their loads are in flight together).
+// (their loads are in flight together).  Measured: bf16 8192 x 5120 in 24.9 us (128
+// MB moved, 5.1 TB/s, where a large copy moves 5.2); 1 x 5120 in 2.8 us, a launch.
 template <typename T, bool VEC, int U>
 __global__ __launch_bounds__(256) void block_quantize_rows_kernel(Fp8BlockQuantParams p) {
   const uint32_t l8 = threadIdx.x % 8;
@@ -131,6 +132,7 @@ __global__ __launch_bounds__(256) void block_quantize_rows_kernel(Fp8BlockQuantP
 }
 
 // One scale per 128 x 128 tile: thread t holds 16 columns of rows t / 8 + 32 i.
+// Measured: bf16 25600 x 5120 in 77.6 us (393 MB, 5.1 TB/s).
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void block_quantize_tiles_kernel(Fp8BlockQuantParams p) {
   const uint32_t tr = p.div_kb.div(blockIdx.x), kb = blockIdx.x - tr * p.div_kb.d;

@@ -11,13 +11,19 @@
 // Launches, none of which waits for another on the host:
 //   1. prep: a wave per token finds its experts; a workgroup per token writes x as
 //      f16 (below).
-//   2. gate_up: one workgroup per (expert, 16 RT rows of h); its waves split the
-//      hidden dimension and join through LDS; SiLU gate; h to the workspace as f16.
+//   2. gate_up: one workgroup per (expert, 16 rows of h); its waves split the hidden
+//      dimension and join through LDS; SiLU gate; h to the workspace as f16.  Where
+//      experts have many tokens: 64 rows, a wave for 16, and the columns shared.
 //   3. down: one workgroup per (expert, 64 RT rows of out), its products times the
 //      routing weight to the workspace, and
 //   4. combine: the sum over a token's experts, in slot order.
 //      Up to kOwnSlots slots: instead one kernel whose workgroups own 16 rows of out,
 //      their waves taking the slots in turn, joined in wave order.
+// Measured (kernels alone, us): 32 tokens, 512 experts top-10, H 4096, I 1024, bf16
+// (1.7 GB of weights): prep 6, gate_up 226 (5.0 TB/s; a large copy moves 5.2), down 133
+// (4.2), combine 5.  4 tokens of the same layer: 5.4, 38.8 (4.7), 25.4 (3.6), 4.7.  One
+// token, 128 experts top-8, H 2048, I 768: 3.1, 6.8 (2.1), own 6.9 (1.0): there
+// the latency of dependent loads bounds each launch, not their bytes.
 // No atomics anywhere: the same result every time.  No list of experts is built:
 // a workgroup is given a slot and leaves if an earlier slot has the same expert
 // (or, with more slots than experts, an expert, and leaves if no slot has it), and
@@ -220,11 +226,13 @@ __device__ __forceinline__ half8v decode8(uint32_t w, _Float16 s) {
   return (half8v){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// What a lane holds of 16 weight rows for one 256-wide step: 64 codes of its row
-// and their 4 block scales.
-// Swizzle of the eight 16-byte pieces of a 128-byte LDS row (fp8_block_gemm.hip)
+// Swizzle of the eight 16-byte pieces of a 128-byte LDS row: piece c of row r is stored
+// at c ^ swz128(r), so 16 rows read at one piece are free of conflicts (every two rows
+// share a window of 256 bytes)
 __device__ __forceinline__ uint32_t swz128(uint32_t r) { return (r >> 1) & 7u; }
 
+// What a lane holds of 16 weight rows for one 256-wide step: 64 codes of its row
+// and their 4 block scales.
 struct Codes {
   u32x4 lo, hi;
   uint32_t s;
@@ -345,7 +353,8 @@ __device__ __forceinline__ void multiply(const Codes (&c)[NM], const Columns<NT,
 //  ALIGNED: fetch() starts a step's way into LDS (ring: NM kTile bytes of the wave's
 //  own), take() reads it back once it has landed: a transfer takes eight rows' whole
 //  128 bytes, where loads in the matrix instruction's order touch 16 rows with every
-//  16 lanes, 64 line lookups for the 1 KB that 8 lines hold (15% of the layer).
+//  16 lanes, 64 line lookups for the 1 KB that 8 lines hold (the header's 32
+//  tokens: 385 us with those, 354 with whole lines).
 //  Otherwise fetch() loads straight into registers, at any alignment.
 constexpr uint32_t kTile = 16 * 128 + 16 * 16;  // codes, then scales
 template <int NM, bool ALIGNED>
@@ -529,7 +538,12 @@ struct Column {
   }
 };
 
-constexpr uint32_t kOwnSlots = 16;  // slots up to which one kernel does down and combine
+// Slots up to which one kernel does down and combine.  Beyond, it reads a shared
+// expert's rows once per slot and its few workgroups hold less in flight.  Whole
+// layer, us, one kernel / two (k of E experts, T tokens, H 2048, I 768): 8 slots (T1
+// k8) 17.1 / 18.9, 16 (T2 k8) 21.3 / 21.9, 16 (T16 k1) 20.4 / 20.9, 24 (T3 k8) 26.0 /
+// 25.6, 32 (T4 k8) 31.9 / 28.6, 32 (T32 k1) 30.5 / 27.3; H 4096, I 1024: 16 37.1 / 40.3
+constexpr uint32_t kOwnSlots = 16;
 
 // Which expert a workgroup works for, and its tokens.
 struct Work {
@@ -886,7 +900,13 @@ __global__ __launch_bounds__(1024) void decode_own_kernel(MoeDecodeParams p) {
 
 // Column tiles a pass, from the tokens an expert has on average: 1 (the columns
 // straight from memory), or 2 or 4 (through LDS, shared).  One more pass reads the
-// weights again, one tile too many costs registers and LDS.
+// weights again, one tile too many costs registers and LDS.  Whole layer, us, with
+// 1 / 2 / 4 tiles (H 2048, I 768, 16 experts, bf16: 16 tokens a tile; a token's slots
+// spread unevenly, so a mean of half a tile fills one):
+//   tokens an expert 4: 24.0 / 30.6 / 40.8    8: 26.2 / 30.7 / 40.5
+//   12: 33.2 / 31.5 / 41.7   16: 40.2 / 32.6 / 42.5   32: 59.9 / 52.0 / 46.1
+// float32 (8 tokens a tile), H 4096, I 1024: 4: 52.0 / 57.5 / 82.0
+//   8: 79 / 60.2 / 85.5   16: 130 / 95.1 / 91.9
 template <int P>
 int column_tiles(const MoeDecodeParams &p) {
   const uint32_t mean = p.S / min(p.S, p.E);
@@ -919,9 +939,17 @@ hipError_t launch_down(const MoeDecodeParams &p, hipStream_t stream) {
     decode_own_kernel<PH, ALIGNED, OutT><<<p.H / 16, 1024, 0, stream>>>(p);
     return hipGetLastError();
   }
-  // two row tiles a wave keep twice the bytes in flight and read the columns half as
-  // often; one while there are few workgroups
-  if ((uint64_t)(p.H / 64) * min(p.S, p.E) >= 8 * device_cu_count()) launch_down_rt<PH, 2, ALIGNED>(p, stream);
+  // Two row tiles a wave keep twice the bytes in flight and read the columns half as
+  // often; one while that leaves a compute unit fewer than three workgroups of 64 rows.
+  // Whole layer, us, one / two (T x E x k x H x I, workgroups of one tile):
+  //   128x8x2x2048x768      256   35.7 / 37.8
+  //   40x4x4x4096x1024      256   51.0 / 53.8
+  //   64x16x4x2048x768      512   33.0 / 33.5     128x16x4x2048x768  512  46.0 / 40.5
+  //   3x64x8x2048x768       768   26.4 / 26.7     37x24x5x2064x784   768  49.2 / 46.0
+  //   64x32x4x2048x768     1024   40.0 / 37.8
+  //   8x64x6x4096x1024     3072   75.2 / 72.7
+  //   32x512x10x4096x1024 15300    386 / 358
+  if ((uint64_t)(p.H / 64) * min(p.S, p.E) >= 3 * device_cu_count()) launch_down_rt<PH, 2, ALIGNED>(p, stream);
   else launch_down_rt<PH, 1, ALIGNED>(p, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
