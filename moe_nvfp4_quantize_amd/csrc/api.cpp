@@ -351,7 +351,7 @@ nvfp4_status nvfp4_fp8_block_gemm(const uint8_t *a_q, const float *a_s, const ui
                                   nvfp4_dtype c_type, int64_t ldc, hipStream_t stream) {
   if (!valid_dtype(c_type) || M < 0 || N < 0 || K <= 0 || K % 16 != 0 || ldc < N)
     return NVFP4_ERR_INVALID_ARG;
-  // a launch's threads (one row of 16 x 16 tiles has 64 per column) stay under 2^32
+  // a launch's threads (32 per column of C at the most) stay under 2^32
   if (M >= (1 << 26) || N >= (1 << 26) || M * N >= (1ll << 38) || K > kI32Max) return NVFP4_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return NVFP4_OK;
   if (!a_q || !a_s || !b_q || !b_s || !c || !aligned16(a_q) || !aligned16(b_q) || ((uintptr_t)a_s & 3u) ||

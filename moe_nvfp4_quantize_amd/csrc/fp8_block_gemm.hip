@@ -110,12 +110,13 @@ __device__ __forceinline__ Fp8Frag load_frag(const uint8_t *row, uint64_t k, uin
   return f;
 }
 
-// A row or a few (and, with 64-bit offsets, any shape): bound by one read of B.  A
+// A row or a few (and, with 64-bit offsets, any number): bound by one read of B.  A
 // workgroup owns 16 columns of 16 rows of C and its NW waves take the 128-column
 // blocks of K in turn, U blocks' loads in flight together, straight into registers
 // (M = 1 reads the same lines of A in every lane group).  The waves' sums are
-// joined through LDS in wave order.  Measured: 1 x 5120 x 5120 in 8.8 us (26 MB, 3.0
-// TB/s): launch, three turns of loads and the join, one after the other.
+// joined through LDS in wave order.  Measured: 1 x 151936 x 2048 in 51 us (311 MB, 6.1
+// TB/s: part of it from the last-level cache), 1 x 4096 x 14336 in 14.1 us (4.2).  (16
+// waves of 2: 67 and 14.6, half of them idle at K 2048; 8 of 4: 66 and 16.6.)
 template <int NW, int U, typename OutT>
 __global__ __launch_bounds__(NW * 64) void block_gemm_rows_kernel(Fp8BlockGemmParams p) {
   __shared__ __attribute__((aligned(16))) float red[NW][16][20];
@@ -178,7 +179,7 @@ __device__ __forceinline__ uint32_t swz128(uint32_t r) { return (r >> 1) & 7u; }
 // work is bound by how fast a compute unit takes in its (32 FM + 32 FN) K bytes,
 // which the depth of the stages (not registers) keeps in flight.  The resources
 // end at the matrix's last row: rows past it cost nothing.  Measured: 32 x 25600 x
-// 5120 in 30 us (133 MB, 4.4 TB/s); 1000 x 1552 x 2064 float32 in 15 us.
+// 5120 in 30 us (133 MB, 4.4 TB/s); 1 x 5120 x 5120 in 7.4 us (26 MB, 3.5 TB/s); 1000 x 1552 x 2064 float32 in 15 us.
 template <int FM, int FN, int NW, int NST, typename OutT>
 __global__ __launch_bounds__(NW * 64, 1) void block_gemm_strip_kernel(Fp8BlockGemmParams p) {
   using Op = Operand<kExact<OutT>>;
@@ -645,7 +646,7 @@ template <typename OutT>
 hipError_t launch_rows(const Fp8BlockGemmParams &p, hipStream_t stream) {
   const uint64_t grid_m = ((uint64_t)p.M + 15) / 16;
   if (grid_m > 65535) return hipErrorInvalidValue;
-  block_gemm_rows_kernel<16, 2, OutT><<<dim3((p.N + 15) / 16, (uint32_t)grid_m), 1024, 0, stream>>>(p);
+  block_gemm_rows_kernel<8, 2, OutT><<<dim3((p.N + 15) / 16, (uint32_t)grid_m), 512, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -663,15 +664,23 @@ hipError_t launch_rows(const Fp8BlockGemmParams &p, hipStream_t stream) {
 //   64 x 5120     32 x 64         10.8   64 x 64 15.2, 32 x 32 13.3
 //   32 x 25600    32 x 128        30.8   32 x 64 33.5
 //   32 x 5120     32 x 32         9.5    32 x 64 11.0
-//   1 x 2048 (K 2048)  rows       4.1    32 x 32 5.1
+//   1 x 5120      32 x 32         7.4    rows 9.0
+// Up to four rows whose 32-column tiles would leave units idle go by 16 columns straight
+// from memory (the rows kernel), and so does a single row while K is one turn of its
+// waves (us, rows / tiles, N x K):
+//   1 row:  2048 x 2048 4.0 / 5.1, 4096 x 14336 14.1 / 20.6, 1024 x 5120 5.5 / 6.8,
+//           25600 x 2048 12.1 / 13.1, 151936 x 2048 51.2 / 59.2, 5120 x 25600 37.2 / 32.3
+//   4 rows: 2048 x 2048 4.2 / 5.1, 4096 x 14336 13.9 / 17.4, 25600 x 2048 13.8 / 13.1
+//   16:     2048 x 2048 4.9 / 5.0, 25600 x 2048 19.1 / 13.9
 // A float32 result (f16 products, converted operands) skips 64 x 128: 1000 x 1552
 // x 2064 takes 15.5 with 64 x 64 and 22.7 with 64 x 128.
 template <typename OutT>
 hipError_t launch_typed(const Fp8BlockGemmParams &p, hipStream_t stream) {
   // the tiles' resources hold up to 256 rows: 32-bit offsets
-  if (p.M <= 4 || (uint64_t)p.K * 256 >= (1ull << 32)) return launch_rows<OutT>(p, stream);
+  if ((uint64_t)p.K * 256 >= (1ull << 32)) return launch_rows<OutT>(p, stream);
   const uint64_t enough = device_cu_count() * 3 / 5;
   auto fills = [&](uint64_t bm, uint64_t bn) { return ((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn) >= enough; };
+  if ((p.M <= 4 && !fills(32, 32)) || (p.M == 1 && p.K <= 2048)) return launch_rows<OutT>(p, stream);
   if (p.M > 64) {
     if (fills(128, 256)) return launch_tile<128, 256, 2, 2, 3, OutT>(p, stream);
     if (fills(128, 128)) return launch_tile<128, 128, 2, 2, 3, OutT>(p, stream);

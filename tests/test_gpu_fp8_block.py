@@ -261,3 +261,11 @@ def test_inputs_freed_behind_a_call_on_another_stream(B):
     side.synchronize()
     assert torch.equal(q, a0[0]) and torch.equal(s, a0[1]) and torch.equal(y, want)
     assert all(torch.all(t == 1) for t in fill)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(1, 4896, 2048), (1, 4897, 2064), (1, 4850, 2064), (4, 4865, 144), (4, 4864, 144),
+                                   (3, 4900, 5136), (1, 20000, 16)])
+def test_gemm_few_rows_both_kernels(B, M, N, K, dtype):
+    """Both sides of the rule for up to four rows."""
+    _check(B, M, N, K, dtype)
