@@ -39,6 +39,8 @@ Modules:
     four_over_six -- weight block scales chosen between maps to 6 and to 4
     qdq      -- quantize then dequantize (fake quantization)
     fp8      -- FP8 E4M3 per-tensor W8A8 quantize, dequantize and GEMM
+    fp8_block -- the same with one scale per block of 128 columns by 1 or 128 rows
+    moe_decode -- the routed-expert layer on activations that are not quantized
 """
 
 from . import formats, nvfp4, gemm, moe  # noqa: F401
