@@ -947,7 +947,7 @@ hipError_t launch_down(const MoeDecodeParams &p, hipStream_t stream) {
   //   64x16x4x2048x768      512   33.0 / 33.5     128x16x4x2048x768  512  46.0 / 40.5
   //   3x64x8x2048x768       768   26.4 / 26.7     37x24x5x2064x784   768  49.2 / 46.0
   //   64x32x4x2048x768     1024   40.0 / 37.8
-  //   8x64x6x4096x1024     3072   75.2 / 72.7
+  //   8x64x8x2048x768      2048   40.9 / 39.3
   //   32x512x10x4096x1024 15300    386 / 358
   if ((uint64_t)(p.H / 64) * min(p.S, p.E) >= 3 * device_cu_count()) launch_down_rt<PH, 2, ALIGNED>(p, stream);
   else launch_down_rt<PH, 1, ALIGNED>(p, stream);

@@ -269,3 +269,61 @@ def test_inputs_freed_behind_a_call_on_another_stream(B):
 def test_gemm_few_rows_both_kernels(B, M, N, K, dtype):
     """Both sides of the rule for up to four rows."""
     _check(B, M, N, K, dtype)
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_offsets_past_32_bits(B, block_rows):
+    """4.3e9 elements: the last rows are what those rows alone give."""
+    rows, cols = 2 ** 21, 2064
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x[:] = torch.arange(cols, device="cuda")
+    tail = slice(rows - 256, rows)
+    x[tail] = _uneven(256, cols, 3, torch.bfloat16)
+    q, s = B.nvfp4_fp8_block_quantize(x, block_rows)
+    want = B.nvfp4_fp8_block_quantize(x[tail], block_rows)
+    assert torch.equal(q[tail], want[0]) and torch.equal(s[-256 // block_rows:], want[1])
+    assert torch.equal(q[:128], q[128 * 1000:128 * 1001])
+
+
+@pytest.mark.parametrize("M", [1, 3, 40, 130])
+def test_gemm_offsets_past_32_bits(B, M):
+    """B of more than 2^32 bytes, and (130 rows) a C that reaches past 2^32 bytes: the last columns."""
+    N, K = 2 ** 25, 144
+    a, _ = _operands(M, 128, K, M)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    bq = torch.randint(0, 0x7F, (N, K), generator=g, device="cuda", dtype=torch.uint8)
+    bs = torch.rand((N // 128, 2), generator=g, device="cuda")
+    y = B.nvfp4_fp8_block_gemm(a, (bq, bs), out_dtype=torch.bfloat16)
+    for c0 in (0, N - 384):
+        args = [t.cpu().numpy() for t in (*a, bq[c0:c0 + 384], bs[c0 // 128:c0 // 128 + 3])]
+        ref, tol = P.gemm(*args), P.gemm_bound(*args, fp8_unit=True)
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+        assert np.all(np.abs(y[:, c0:c0 + 384].double().cpu().numpy() - ref) <= tol)
+
+
+@pytest.mark.parametrize("M", [5, 70])
+def test_gemm_long_rows_offsets(B, M):
+    """Rows so long that few of them pass 2^32 bytes, on both sides of where the tiles' offsets end."""
+    for N, K in ((300, 2 ** 24 - 16), (260, 2 ** 24 + 16)):
+        a, b = _operands(M, 128, 256, M)
+        aq = torch.zeros((M, K), dtype=torch.uint8, device="cuda")
+        bq = torch.zeros((N, K), dtype=torch.uint8, device="cuda")
+        kb = -(-K // 128)
+        as_ = torch.ones((M, kb), device="cuda")
+        bs = torch.ones((-(-N // 128), kb), device="cuda")
+        g = torch.Generator(device="cuda")
+        g.manual_seed(N)
+        cols = torch.tensor([0, 16, 4096, K // 2, K - 16], device="cuda")[:, None] + torch.arange(16, device="cuda")
+        cols = cols.reshape(-1)
+        aq[:, cols] = torch.randint(0, 0x7F, (M, cols.numel()), generator=g, device="cuda", dtype=torch.uint8)
+        bq[:, cols] = torch.randint(0, 0x7F, (N, cols.numel()), generator=g, device="cuda", dtype=torch.uint8)
+        y = B.nvfp4_fp8_block_gemm((aq, as_), (bq, bs), out_dtype=torch.float32)
+        # unit scales: the same product over the 80 columns that hold anything.  Adding zeros is exact,
+        # so an output rounds at most 32 + 5 + 5 + 3 times (codes of a block, blocks, waves, scales),
+        # fewer than the 80 + 1 + 3 that the bound of the dense product counts
+        small = [aq[:, cols].cpu().numpy(), np.ones((M, 1), np.float32), bq[:, cols].cpu().numpy(),
+                 np.ones((-(-N // 128), 1), np.float32)]
+        ref, tol = P.gemm(*small), P.gemm_bound(*small)
+        assert np.all(np.abs(y.double().cpu().numpy() - ref) <= tol)
+        del aq, bq, as_, bs

@@ -226,3 +226,17 @@ def test_one_expert_for_a_whole_batch(B):
         logits[:] = 0.0
         logits[:, E - 1] = 5.0
         _check(B.nvfp4_moe_decode(x, logits, k, gu, dn, out_dtype=torch.float32), x, logits, k, gu, dn)
+
+
+@pytest.mark.parametrize("T", [1, 20])
+def test_offsets_past_32_bits(B, T):
+    """1024 experts whose codes pass 2^32 bytes, the last ones routed to: as with those alone."""
+    E, k, H, I = 1024, 2, 2048, 2112
+    gu, dn = _weights(E, 2 * I, H, 4), _weights(E, H, I, 5)
+    assert gu[0].numel() > 2 ** 32
+    x = W.random_matrix(T, H, seed=1, dtype=torch.bfloat16, device="cuda")
+    logits = torch.full((T, E), -50.0, device="cuda")
+    logits[:, -5:] = W.random_matrix(T, 5, seed=2, device="cuda")
+    last = [tuple(t[-5:].contiguous() for t in w) for w in (gu, dn)]
+    y = B.nvfp4_moe_decode(x, logits, k, gu, dn, out_dtype=torch.float32)
+    _check(y, x, logits[:, -5:], k, *last)
