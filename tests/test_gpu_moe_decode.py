@@ -240,3 +240,26 @@ def test_offsets_past_32_bits(B, T):
     last = [tuple(t[-5:].contiguous() for t in w) for w in (gu, dn)]
     y = B.nvfp4_moe_decode(x, logits, k, gu, dn, out_dtype=torch.float32)
     _check(y, x, logits[:, -5:], k, *last)
+
+
+def test_captured_on_a_given_stream(B):
+    """A capture whose calls name its stream: replays with eager work on the default stream
+    between them equal the eager result."""
+    x, logits, k, gu, dn = _case(9, 16, 3, 256, 128, 4)
+    y = torch.empty((9, 256), device="cuda")
+    side = torch.cuda.Stream()
+    w = B.nvfp4_fp8_block_quantize(W.random_matrix(300, 256, seed=5, device="cuda"), 128)
+    z = torch.empty((9, 300), device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        B.nvfp4_moe_decode(x, logits, k, gu, dn, out=y, stream=side)
+        B.nvfp4_fp8_block_gemm(B.nvfp4_fp8_block_quantize(y, stream=side), w, out=z, stream=side)
+    for i in range(3):
+        x.copy_(W.random_matrix(9, 256, seed=70 + i, device="cuda"))
+        want = B.nvfp4_moe_decode(x, logits, k, gu, dn, out_dtype=torch.float32)
+        want_z = B.nvfp4_fp8_block_gemm(B.nvfp4_fp8_block_quantize(want), w, out_dtype=torch.float32)
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(z, want_z), i
